@@ -25,7 +25,8 @@
  * dense-gradient mode (emb_bag_bwd_dense_grad, emb_nobag_bwd_dense_grad), the
  * forward pooled lookup (emb_bag_fwd), an allocation-free unpooled update
  * (emb_nobag_bwd_sgd_atomic_noalloc), and the exchange step of row-sharded
- * tables over several ranks (emb_shard_*). emb_shard_bucketize is the one call
+ * tables over several ranks (emb_shard_*), and the vocabulary operators of a
+ * language model (emb_logits_process, emb_distill_*, emb_micro_*). emb_shard_bucketize is the one call
  * that synchronises (it returns the exchange's split sizes).
  *
  * Layouts (all element offsets, not bytes):
@@ -354,6 +355,119 @@ emb_status emb_shard_merge(emb_shard* shard, const int64_t* recv_offsets, const 
 
 /* Waits for the shard's last call and returns (and clears) its latched errors. */
 emb_status emb_shard_status(emb_shard* shard);
+
+/* ---- Vocabulary operators of a language model: its token table is also the matrix
+ * of its output logits. They need no plan and no workspace, allocate nothing and
+ * never synchronise, so they can be captured in a CUDA graph. `device` is the CUDA
+ * device of the pointers and of `stream`. Row strides are in elements and matter
+ * where there is more than one row. Argument errors are returned synchronously.
+ * device_status (device uint32, may be NULL) collects device error bits: they are
+ * added to it (the caller clears it) - 1 = an id outside its range (the entry is
+ * left out), 2 = malformed CSR offsets (the list is taken as empty), 4 = a bounded
+ * wait ran out (the output is not valid). */
+
+/* Logits before a token is chosen. B requests (<= 65535), V tokens (<= 2^20). For
+ * token v of request b, with z its logit and c the times v occurs in the request's
+ * output ids:
+ *   v in the prompt or output ids:  z <- z > 0 ? z / repetition[b] : z * repetition[b]
+ *   v in the output ids:            z <- z - frequency[b] * c - presence[b]
+ *   z <- z + the biases of v, in the order of the list
+ *   bit v % 32 of mask[b, v / 32] clear:  z <- -infinity
+ * in fp32, rounded once to out_dtype. prompt/output/bias lists are CSR: ids int64[n],
+ * offsets int64[B+1] with values in 0..n (both NULL and n = 0: no list; a bias list
+ * has fp32 bias_values). repetition, frequency, presence: fp32[B], NULL = 1, 0, 0.
+ * mask: uint32 [B, mask_stride >= ceil(V / 32)] or NULL. `out` may be `logits` itself
+ * (same type and stride), and must not overlap it otherwise. */
+emb_status emb_logits_process(int device, const void* logits, emb_dtype logits_dtype,
+                              int64_t logits_stride, int32_t B, int32_t V,
+                              const int64_t* prompt_ids, const int64_t* prompt_offsets,
+                              int64_t prompt_n, const int64_t* output_ids,
+                              const int64_t* output_offsets, int64_t output_n,
+                              const float* repetition, const float* frequency,
+                              const float* presence, const int64_t* bias_ids,
+                              const int64_t* bias_offsets, const float* bias_values,
+                              int64_t bias_n, const uint32_t* mask, int64_t mask_stride, void* out,
+                              emb_dtype out_dtype, int64_t out_stride, uint32_t* device_status,
+                              void* stream);
+
+/* Distillation from a teacher's top logits. Row n of the student's logits z [N, V]
+ * (V <= 2^20), tau = temperature > 0, p = softmax(z / tau), and the teacher's list of
+ * K <= 1024 entries (teacher_ids int64, teacher_logits; row stride teacher_stride for
+ * both), q_k = exp(t_k / tau - L):
+ *   teacher_lse given (fp32[N], L = log of the teacher's whole sum of exp(t / tau)):
+ *     r = max(0, 1 - sum q), u = mass of p off the list,
+ *     loss = tau^2 * (sum_k q_k (log q_k - log p_{id_k}) + r (log r - log u))
+ *   teacher_lse NULL: L = log sum_k exp(t_k / tau) and r = 0.
+ *   d loss / d z_v = tau * (p_v - q of the entries with id v)   on the list,
+ *                    tau * p_v * (1 - r / u)                    off it.
+ * Entries with id -1 are padding. Rows without entries, and rows with L = -infinity (a
+ * teacher without mass), have loss 0 and gradient 0. Entries that repeat an id add.
+ *   emb_distill_forward   loss fp32[N]; stats fp32[N, 4], 16-byte aligned: {largest z,
+ *                         sum of exp((z - largest) / tau), 1 - r / u, L}
+ *   emb_distill_backward  dlogits (logits_dtype) = row_weight[n] * dloss/dz from the
+ *                         forward's stats; row_weight fp32[N] or NULL = 1
+ *   emb_distill_step      loss and dlogits in one call, for a row_weight known
+ *                         beforehand; z is read once where a row fits on chip
+ * dlogits may be logits itself (same stride) and must not overlap it otherwise. */
+emb_status emb_distill_forward(int device, const void* logits, emb_dtype logits_dtype,
+                               int64_t logits_stride, int32_t N, int32_t V,
+                               const int64_t* teacher_ids, const void* teacher_logits,
+                               emb_dtype teacher_dtype, int64_t teacher_stride, int32_t K,
+                               const float* teacher_lse, float temperature, float* loss,
+                               float* stats, uint32_t* device_status, void* stream);
+emb_status emb_distill_backward(int device, const void* logits, emb_dtype logits_dtype,
+                                int64_t logits_stride, int32_t N, int32_t V,
+                                const int64_t* teacher_ids, const void* teacher_logits,
+                                emb_dtype teacher_dtype, int64_t teacher_stride, int32_t K,
+                                const float* stats, const float* row_weight, float temperature,
+                                void* dlogits, int64_t dlogits_stride, uint32_t* device_status,
+                                void* stream);
+emb_status emb_distill_step(int device, const void* logits, emb_dtype logits_dtype,
+                            int64_t logits_stride, int32_t N, int32_t V,
+                            const int64_t* teacher_ids, const void* teacher_logits,
+                            emb_dtype teacher_dtype, int64_t teacher_stride, int32_t K,
+                            const float* teacher_lse, const float* row_weight, float temperature,
+                            float* loss, void* dlogits, int64_t dlogits_stride,
+                            uint32_t* device_status, void* stream);
+
+/* Microscaled 4-bit floating point: E2M1 elements (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ * negatives) with a scale for every block.
+ *   EMB_MICRO_MX: blocks of 32 share 2^(byte - 127), exponent floor(log2(amax)) - 2 (at
+ *     least -127); byte 255 = NaN. No tensor scale (pass 1).
+ *   EMB_MICRO_NV: blocks of 16 share an E4M3 scale times the tensor's fp32 scale g
+ *     (1e-15..1e15): E4M3(amax / (6 g)), saturating.
+ * An element is multiplied by the scale's reciprocal (rounded to fp32; exact for MX), rounded
+ * to the nearest even code and saturates at 6. A block that holds an
+ * infinity or a NaN gets a NaN scale: all its elements read back as NaN.
+ * codes: [rows, 16 * ceil(K / 32)] bytes; element k in bits 0-3 (k even) or 4-7 (k odd)
+ *   of byte k / 2; padded with zeros.
+ * scales: tiles of 512 bytes for 128 rows x 4 blocks, tile (i, j) at (i * ceil(blocks / 4)
+ *   + j) * 512 with blocks = ceil(K / 32) * (MX: 1, NV: 2); block j of row r at byte
+ *   (r % 32) * 16 + (r % 128 / 32) * 4 + j % 4 of tile (r / 128, j / 4); padded with zeros.
+ * Both 16-byte aligned, and written entirely by emb_micro_quantize. K <= 2^20. */
+typedef enum { EMB_MICRO_MX = 0, EMB_MICRO_NV = 1 } emb_micro_format;
+
+/* x [R, K] -> codes, scales. */
+emb_status emb_micro_quantize(int device, const void* x, emb_dtype x_dtype, int64_t x_stride,
+                              int64_t R, int32_t K, emb_micro_format format, float tensor_scale,
+                              uint8_t* codes, uint8_t* scales, void* stream);
+
+/* Rows ids[0..n) of a microscaled table of R rows as values, out [n, K]: code * block
+ * scale * tensor scale, rounded once to out_dtype. ids NULL: rows 0..n-1 (n <= R). An id
+ * outside the table gives a row of zeros and error bit 1. */
+emb_status emb_micro_lookup(int device, const uint8_t* codes, const uint8_t* scales, int64_t R,
+                            int32_t K, emb_micro_format format, float tensor_scale,
+                            const int64_t* ids, int64_t n, void* out, emb_dtype out_dtype,
+                            int64_t out_stride, uint32_t* device_status, void* stream);
+
+/* out[m, n] = sum_k X[m, k] * W[n, k] for microscaled X [M, K] and W [N, K] of one format
+ * (M, N <= 2^21), summed in fp32 and rounded once: the logits of M hidden states against
+ * a table of N tokens. */
+emb_status emb_micro_matmul(int device, const uint8_t* x_codes, const uint8_t* x_scales,
+                            float x_tensor_scale, int32_t M, const uint8_t* w_codes,
+                            const uint8_t* w_scales, float w_tensor_scale, int32_t N, int32_t K,
+                            emb_micro_format format, void* out, emb_dtype out_dtype,
+                            int64_t out_stride, uint32_t* device_status, void* stream);
 
 /* Static description of a status code. */
 const char* emb_status_string(emb_status status);

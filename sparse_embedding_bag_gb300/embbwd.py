@@ -21,6 +21,7 @@ EMB_ERR_OOM, EMB_ERR_CUDA, EMB_ERR_TIMEOUT = 4, 5, 6
 EMB_F32, EMB_F16, EMB_BF16 = 0, 1, 2
 EMB_POOL_SUM, EMB_POOL_MEAN = 0, 1
 EMB_NOBAG_AUTO, EMB_NOBAG_SORTED, EMB_NOBAG_ATOMIC = 0, 1, 2
+EMB_MICRO_MX, EMB_MICRO_NV = 0, 1
 EMB_FLAG_CHECK_INDICES = 0x1
 EMB_FLAG_NO_PDL = 0x2
 EMB_FLAG_STOCHASTIC_ROUNDING = 0x4
@@ -34,7 +35,9 @@ EXPORTS = ("emb_bwd_plan", "emb_plan_destroy", "emb_bag_bwd_sgd", "emb_bag_bwd_r
            "emb_bag_fwd", "emb_bag_bwd_adagrad", "emb_bag_bwd_dense_grad",
            "emb_nobag_bwd_dense_grad", "emb_plan_set_rounding", "emb_plan_get_rounding",
            "emb_shard_create", "emb_shard_create_cyclic", "emb_shard_destroy", "emb_shard_bucketize",
-           "emb_shard_merge", "emb_shard_status")
+           "emb_shard_merge", "emb_shard_status", "emb_logits_process", "emb_distill_forward",
+           "emb_distill_backward", "emb_distill_step", "emb_micro_quantize", "emb_micro_lookup",
+           "emb_micro_matmul")
 
 _lock = threading.Lock()
 _lib = None
@@ -82,6 +85,18 @@ def load(path: str = LIB_PATH):
             "emb_shard_bucketize": [vp, vp, vp, i64, i32, vp, c_int, vp, vp, vp, vp, vp],
             "emb_shard_merge": [vp, vp, vp, vp, i64, i32, vp, vp, vp, vp],
             "emb_shard_status": [vp],
+            "emb_logits_process": [c_int, vp, c_int, i64, i32, i32, vp, vp, i64, vp, vp, i64, vp, vp, vp,
+                                   vp, vp, vp, i64, vp, i64, vp, c_int, i64, vp, vp],
+            "emb_distill_forward": [c_int, vp, c_int, i64, i32, i32, vp, vp, c_int, i64, i32, vp, f32,
+                                    vp, vp, vp, vp],
+            "emb_distill_backward": [c_int, vp, c_int, i64, i32, i32, vp, vp, c_int, i64, i32, vp, vp,
+                                     f32, vp, i64, vp, vp],
+            "emb_distill_step": [c_int, vp, c_int, i64, i32, i32, vp, vp, c_int, i64, i32, vp, vp, f32,
+                                 vp, vp, i64, vp, vp],
+            "emb_micro_quantize": [c_int, vp, c_int, i64, i64, i32, c_int, f32, vp, vp, vp],
+            "emb_micro_lookup": [c_int, vp, vp, i64, i32, c_int, f32, vp, i64, vp, c_int, i64, vp, vp],
+            "emb_micro_matmul": [c_int, vp, vp, f32, i32, vp, vp, f32, i32, i32, c_int, vp, c_int, i64,
+                                 vp, vp],
         }
         for name, args in sig.items():
             fn = getattr(lib, name)
@@ -312,3 +327,76 @@ def emb_shard_merge(shard, recv_offsets, recv_indices, recv_scales, n_recv, B, m
 
 def emb_shard_status(shard):
     return load().emb_shard_status(shard)
+
+
+# ---- vocabulary operators (vocab.py calls these with tensors checked and outputs made)
+
+def emb_logits_process(device, logits, logits_dtype, logits_stride, B, V, prompt_ids, prompt_offsets,
+                       prompt_n, output_ids, output_offsets, output_n, repetition, frequency,
+                       presence, bias_ids, bias_offsets, bias_values, bias_n, mask, mask_stride, out,
+                       out_dtype, out_stride, device_status=None, stream=None):
+    st = load().emb_logits_process(device, _ptr(logits), logits_dtype, logits_stride, B, V,
+                                   _ptr(prompt_ids), _ptr(prompt_offsets), prompt_n,
+                                   _ptr(output_ids), _ptr(output_offsets), output_n,
+                                   _ptr(repetition), _ptr(frequency), _ptr(presence),
+                                   _ptr(bias_ids), _ptr(bias_offsets), _ptr(bias_values), bias_n,
+                                   _ptr(mask), mask_stride, _ptr(out), out_dtype, out_stride,
+                                   _ptr(device_status), _stream(stream))
+    return _check(st, "emb_logits_process")
+
+
+def emb_distill_forward(device, logits, logits_dtype, logits_stride, N, V, teacher_ids,
+                        teacher_logits, teacher_dtype, teacher_stride, K, teacher_lse, temperature,
+                        loss, stats, device_status=None, stream=None):
+    st = load().emb_distill_forward(device, _ptr(logits), logits_dtype, logits_stride, N, V,
+                                    _ptr(teacher_ids), _ptr(teacher_logits), teacher_dtype,
+                                    teacher_stride, K, _ptr(teacher_lse), temperature, _ptr(loss),
+                                    _ptr(stats), _ptr(device_status), _stream(stream))
+    return _check(st, "emb_distill_forward")
+
+
+def emb_distill_backward(device, logits, logits_dtype, logits_stride, N, V, teacher_ids,
+                         teacher_logits, teacher_dtype, teacher_stride, K, stats, row_weight,
+                         temperature, dlogits, dlogits_stride, device_status=None, stream=None):
+    st = load().emb_distill_backward(device, _ptr(logits), logits_dtype, logits_stride, N, V,
+                                     _ptr(teacher_ids), _ptr(teacher_logits), teacher_dtype,
+                                     teacher_stride, K, _ptr(stats), _ptr(row_weight), temperature,
+                                     _ptr(dlogits), dlogits_stride, _ptr(device_status),
+                                     _stream(stream))
+    return _check(st, "emb_distill_backward")
+
+
+def emb_distill_step(device, logits, logits_dtype, logits_stride, N, V, teacher_ids, teacher_logits,
+                     teacher_dtype, teacher_stride, K, teacher_lse, row_weight, temperature, loss,
+                     dlogits, dlogits_stride, device_status=None, stream=None):
+    st = load().emb_distill_step(device, _ptr(logits), logits_dtype, logits_stride, N, V,
+                                 _ptr(teacher_ids), _ptr(teacher_logits), teacher_dtype,
+                                 teacher_stride, K, _ptr(teacher_lse), _ptr(row_weight),
+                                 temperature, _ptr(loss), _ptr(dlogits), dlogits_stride,
+                                 _ptr(device_status), _stream(stream))
+    return _check(st, "emb_distill_step")
+
+
+def emb_micro_quantize(device, x, x_dtype, x_stride, R, K, format, tensor_scale, codes, scales,
+                       stream=None):
+    st = load().emb_micro_quantize(device, _ptr(x), x_dtype, x_stride, R, K, format, tensor_scale,
+                                   _ptr(codes), _ptr(scales), _stream(stream))
+    return _check(st, "emb_micro_quantize")
+
+
+def emb_micro_lookup(device, codes, scales, R, K, format, tensor_scale, ids, n, out, out_dtype,
+                     out_stride, device_status=None, stream=None):
+    st = load().emb_micro_lookup(device, _ptr(codes), _ptr(scales), R, K, format, tensor_scale,
+                                 _ptr(ids), n, _ptr(out), out_dtype, out_stride,
+                                 _ptr(device_status), _stream(stream))
+    return _check(st, "emb_micro_lookup")
+
+
+def emb_micro_matmul(device, x_codes, x_scales, x_tensor_scale, M, w_codes, w_scales,
+                     w_tensor_scale, N, K, format, out, out_dtype, out_stride, device_status=None,
+                     stream=None):
+    st = load().emb_micro_matmul(device, _ptr(x_codes), _ptr(x_scales), x_tensor_scale, M,
+                                 _ptr(w_codes), _ptr(w_scales), w_tensor_scale, N, K, format,
+                                 _ptr(out), out_dtype, out_stride, _ptr(device_status),
+                                 _stream(stream))
+    return _check(st, "emb_micro_matmul")
