@@ -373,8 +373,8 @@ emb_status emb_shard_status(emb_shard* shard);
  *   v in the output ids:            z <- z - frequency[b] * c - presence[b]
  *   z <- z + the biases of v, in the order of the list
  *   bit v % 32 of mask[b, v / 32] clear:  z <- -infinity
- * in fp32, rounded once to out_dtype. prompt/output/bias lists are CSR: ids int64[n],
- * offsets int64[B+1] with values in 0..n (both NULL and n = 0: no list; a bias list
+ * in fp32 (the division as a product with the reciprocal), rounded once to out_dtype.
+ * prompt/output/bias lists are CSR: ids int64[n], n < 2^31, offsets int64[B+1] with values in 0..n (both NULL and n = 0: no list; a bias list
  * has fp32 bias_values). repetition, frequency, presence: fp32[B], NULL = 1, 0, 0.
  * mask: uint32 [B, mask_stride >= ceil(V / 32)] or NULL. `out` may be `logits` itself
  * (same type and stride), and must not overlap it otherwise. */

@@ -7,20 +7,32 @@
 //   y = y - freq_b * c - pres_b * [c > 0] + (sum of the biases of v)
 //   y = -inf where bit v % 32 of mask word v / 32 is clear
 //
-// A block takes a slice of one request's vocabulary. It counts the history's
-// tokens that fall into the slice in shared memory (bit 31: seen in the prompt;
-// the low bits: times in the output; integer atomics, so the counts do not depend
-// on their order), then passes over the slice once. Biases come last, each by one
-// thread that computes its token anew.
+// A block takes a slice of one request's vocabulary. It counts the tokens of its slice in
+// the request's history in shared memory (integer atomics, so that their order does not
+// matter): bit 31 seen in the prompt, bit 30 has a bias, the low bits times in the output.
+// Then it passes over its slice once, eight tokens a thread and step, whose first loads
+// went out before the counting; last come the biased tokens, which the pass left alone.
+//
+// Bound: HBM traffic without lists (512 x 131071 bf16 to bf16: 42 us, 6400 GB/s); with
+// histories of 4000 ids 87 us, bound by instructions: every slice's block reads the
+// whole history (8 slices a row). Measured and dropped: the history shared out over a
+// cluster that counts through distributed shared memory (157 us), a second kernel that
+// rewrites only the listed tokens from a hash table (123 us: scattered reads and partial
+// sectors from HBM), a list of the distinct tokens of a slice (115 us: atomics that
+// return), slices of 8192 tokens (114 us).
 #include <cmath>
 
-#include "vocab.cuh"
+#include "sm103.cuh"
 
 namespace embbwd {
 namespace {
 
-constexpr int kSlice = 8192;  // tokens of one block
-constexpr uint32_t kPromptBit = 0x80000000u;
+constexpr uint32_t kPromptBit = 0x80000000u, kBiasBit = 0x40000000u;  // of a token's count
+constexpr uint32_t kCountBits = kBiasBit - 1;
+constexpr int kMinLogSlice = 11, kMaxLogSlice = 14;  // tokens of a block, a power of two
+constexpr int kLogitThreads = 256, kLogitBlocks = 3;
+constexpr int kGroup = 8;                            // tokens of a thread and step
+constexpr int kBatch = 4;                            // steps whose loads are in flight together
 
 struct LogitsArgs {
   const void* z;
@@ -33,6 +45,7 @@ struct LogitsArgs {
   const uint32_t* mask;
   int64_t mask_stride;
   uint32_t* status;
+  int log_slice;
 };
 
 // [start, end) of request b's list, empty (and reported) if the offsets are malformed.
@@ -46,74 +59,247 @@ __device__ __forceinline__ void list_of(const int64_t* off, int64_t n, int32_t b
   }
 }
 
-__device__ __forceinline__ float penalised(float z, uint32_t c, float rep, float freq, float pres) {
-  if (c == 0) return z;
-  float y = z > 0.f ? __fdiv_rn(z, rep) : z * rep;
-  const uint32_t n = c & ~kPromptBit;
-  if (n) y = (y - __fmul_rn(freq, (float)n)) - pres;
-  return y;
+// The request's penalties. A division by `repetition` is a multiplication by its
+// reciprocal (one more rounding in fp32), and nothing branches: a warp's 256 tokens are
+// rarely all unseen, and a branch for each with a division behind it cost 20 us at
+// 512 x 131071.
+struct Penalty {
+  float rep, inv, freq, pres;
+  __device__ __forceinline__ float operator()(float z, uint32_t c) const {
+    const uint32_t n = c & kCountBits;
+    const float y = c & ~kBiasBit ? z * (z > 0.f ? inv : rep) : z;
+    return n ? fmaf(-freq, (float)n, y) - pres : y;
+  }
+};
+
+// Eight consecutive elements, 16-byte aligned: the load and the widening apart.
+template <typename T>
+struct Raw8 {
+  static constexpr int n = 16 / sizeof(T);
+  uint4 u[kGroup / n];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < kGroup / n; ++i) u[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+  __device__ __forceinline__ void widen(float (&x)[kGroup]) const {
+#pragma unroll
+    for (int i = 0; i < kGroup / n; ++i) {
+      const T* e = reinterpret_cast<const T*>(&u[i]);
+#pragma unroll
+      for (int k = 0; k < n; ++k) x[i * n + k] = Elem<T>::get(e[k]);
+    }
+  }
+};
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&x)[kGroup]) {
+  constexpr int n = 16 / sizeof(T);
+#pragma unroll
+  for (int i = 0; i < kGroup / n; ++i) {
+    uint4 u;
+    T* e = reinterpret_cast<T*>(&u);
+#pragma unroll
+    for (int k = 0; k < n; ++k) e[k] = Elem<T>::put(x[i * n + k]);
+    reinterpret_cast<uint4*>(p)[i] = u;
+  }
 }
 
-template <typename in_t, typename out_t>
-__global__ void __launch_bounds__(kThreads) k_logits(LogitsArgs a) {
-  __shared__ uint32_t count[kSlice];
+// Counts a token in shared memory if off < len. Predicated: a warp's 32 ids rarely miss a
+// slice all together, and a branch around every atomic costs more than the atomic.
+template <bool kOutput>
+__device__ __forceinline__ void count_token(uint32_t count, uint32_t off, uint32_t len) {
+  if (kOutput)
+    asm volatile("{ .reg .pred p; setp.lt.u32 p, %0, %1; @p red.shared.add.u32 [%2], 1; }" ::"r"(off), "r"(len),
+                 "r"(count + off * 4)
+                 : "memory");
+  else
+    asm volatile("{ .reg .pred p; setp.lt.u32 p, %0, %1; @p red.shared.or.b32 [%2], %3; }" ::"r"(off), "r"(len),
+                 "r"(count + off * 4), "r"(kPromptBit)
+                 : "memory");
+}
+
+// Counts the tokens [v0, v0 + len) among n ids at count[v - v0]; returns whether an id is
+// outside the vocabulary. An id is compared by its halves: the high one has to be 0.
+template <bool kOutput>
+__device__ __forceinline__ bool count_ids(const int64_t* ids, int32_t n, uint32_t V, uint32_t v0, uint32_t len,
+                                          uint32_t count) {
+  constexpr int kAhead = 8;  // ids in flight
+  const uint2* p = reinterpret_cast<const uint2*>(ids) + threadIdx.x;
+  uint32_t high = 0, most = 0;  // over all ids
+  auto one = [&](uint2 id) {
+    high |= id.y;
+    most = max(most, id.x);
+    count_token<kOutput>(count, id.y ? 0xffffffffu : id.x - v0, len);
+  };
+  int32_t left = n;  // the same for the whole block
+  for (; left >= kLogitThreads * kAhead; left -= kLogitThreads * kAhead, p += kLogitThreads * kAhead) {
+    uint2 id[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) id[k] = __ldg(p + k * kLogitThreads);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) one(id[k]);
+  }
+  if (left > 0) {
+    uint2 id[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if ((int)threadIdx.x + k * kLogitThreads < left) id[k] = __ldg(p + k * kLogitThreads);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if ((int)threadIdx.x + k * kLogitThreads < left) one(id[k]);
+  }
+  return high != 0 || most >= V;
+}
+
+template <typename in_t, typename out_t, bool kLists>
+__global__ void __launch_bounds__(kLogitThreads, kLogitBlocks) k_logits(LogitsArgs a) {
+  extern __shared__ __align__(16) uint32_t smem[];
+  __shared__ int repeated;  // a bias list names a token twice
   const int32_t b = blockIdx.y;
-  const int32_t v0 = blockIdx.x * kSlice, v1 = min(a.V, v0 + kSlice);
-  for (int i = threadIdx.x; i < kSlice; i += kThreads) count[i] = 0;
-  __syncthreads();
-  for (int part = 0; part < 2; ++part) {
-    const int64_t* ids = part ? a.o_ids : a.p_ids;
-    if (!ids) continue;
-    int64_t s, e;
-    list_of(part ? a.o_off : a.p_off, part ? a.o_n : a.p_n, b, a.status, &s, &e);
-    for (int64_t i = s + threadIdx.x; i < e; i += kThreads) {
-      const int64_t v = ids[i];
-      if (v < 0 || v >= a.V) {
-        report(a.status, kErrIndex);
-      } else if (v >= v0 && v < v1) {
-        if (part) atomicAdd(&count[v - v0], 1u);
-        else atomicOr(&count[v - v0], kPromptBit);
+  const int32_t slice = 1 << a.log_slice;
+  const int32_t v0 = (int32_t)blockIdx.x << a.log_slice, len = min(a.V - v0, slice);
+  const in_t* z = static_cast<const in_t*>(a.z) + b * a.z_stride + v0;
+  out_t* y = static_cast<out_t*>(a.y) + b * a.y_stride + v0;
+  // Groups of eight start `head` tokens into the slice, so that stores are 16-byte
+  // aligned, and loads too where input and output allow it together.
+  constexpr uint32_t in_n = 16 / sizeof(in_t), out_n = 16 / sizeof(out_t), both_n = in_n < out_n ? in_n : out_n;
+  const uint32_t in_at = (uint32_t)(reinterpret_cast<uintptr_t>(z) / sizeof(in_t)) % in_n;
+  const uint32_t out_at = (uint32_t)(reinterpret_cast<uintptr_t>(y) / sizeof(out_t)) % out_n;
+  const bool wide_loads = in_at % both_n == out_at % both_n;
+  const int32_t head = min(len, (int32_t)(wide_loads && in_n > out_n ? -in_at % in_n : -out_at % out_n));
+  const int32_t groups = (len - head) / kGroup;
+  uint32_t* count = smem + (-head & 3);  // groups' counts are 16-byte aligned
+  const uint32_t* mask = a.mask ? a.mask + b * a.mask_stride : nullptr;
+  const float rep = a.rep ? a.rep[b] : 1.f;
+  const Penalty penalty{rep, __frcp_rn(rep), a.freq ? a.freq[b] : 0.f, a.pres ? a.pres[b] : 0.f};
+  int64_t ps = 0, pe = 0, os = 0, oe = 0, bs = 0, be = 0;
+  if (kLists) {
+    if (a.p_ids) list_of(a.p_off, a.p_n, b, a.status, &ps, &pe);
+    if (a.o_ids) list_of(a.o_off, a.o_n, b, a.status, &os, &oe);
+    if (a.b_ids) list_of(a.b_off, a.b_n, b, a.status, &bs, &be);
+  }
+  auto allowed = [&](uint32_t v) { return !mask || (mask[v >> 5] >> (v & 31) & 1u); };
+  // kBatch groups a thread are in flight; the first go out before the lists are read.
+  const in_t* zg = z + head;
+  out_t* yg = y + head;
+  Raw8<in_t> raw[kBatch];
+  uint2 words[kBatch];
+  auto load = [&](int u, int32_t i) {
+    if (i >= groups) return;
+    if (wide_loads) raw[u].load(zg + i * kGroup);
+    if (mask) {
+      const int32_t v = v0 + head + i * kGroup;
+      words[u].x = mask[v >> 5];
+      words[u].y = mask[(v + kGroup - 1) >> 5];
+    }
+  };
+#pragma unroll
+  for (int u = 0; u < kBatch; ++u) load(u, threadIdx.x + u * kLogitThreads);
+  if (kLists) {
+    uint4* c4 = reinterpret_cast<uint4*>(smem);
+    for (int32_t i = threadIdx.x; i < slice / 4 + 1; i += kLogitThreads) c4[i] = make_uint4(0, 0, 0, 0);
+    if (threadIdx.x == 0) repeated = 0;
+    __syncthreads();
+    bool bad = count_ids<false>(a.p_ids + ps, (int32_t)(pe - ps), a.V, v0, len, smem_u32(count));
+    bad |= count_ids<true>(a.o_ids + os, (int32_t)(oe - os), a.V, v0, len, smem_u32(count));
+    for (int64_t j = bs + threadIdx.x; j < be; j += kLogitThreads) {
+      const int64_t v = a.b_ids[j];
+      bad |= v < 0 || v >= a.V;
+      if (v >= v0 && v < v0 + len && (atomicOr(&count[v - v0], kBiasBit) & kBiasBit)) repeated = 1;
+    }
+    if (bad) report(a.status, kErrIndex);
+    __syncthreads();
+  }
+  for (int32_t i0 = threadIdx.x; i0 < groups; i0 += kBatch * kLogitThreads) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int32_t i = i0 + u * kLogitThreads;
+      if (i >= groups) break;
+      float x[kGroup];
+      if (wide_loads) {
+        raw[u].widen(x);
+      } else {
+#pragma unroll
+        for (int k = 0; k < kGroup; ++k) x[k] = Elem<in_t>::get(zg[i * kGroup + k]);
+      }
+      const uint32_t keep = mask ? __funnelshift_r(words[u].x, words[u].y, v0 + head + i * kGroup) : ~0u;
+      load(u, i + kBatch * kLogitThreads);
+      uint32_t any = 0;
+      if (kLists) {
+        const uint4* c4 = reinterpret_cast<const uint4*>(count + head + i * kGroup);
+        const uint4 lo = c4[0], hi = c4[1];
+        any = lo.x | lo.y | lo.z | lo.w | hi.x | hi.y | hi.z | hi.w;
+        if (any) {
+          const uint32_t c[kGroup] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+          for (int k = 0; k < kGroup; ++k) x[k] = penalty(x[k], c[k]);
+        }
+      }
+      if (mask) {
+#pragma unroll
+        for (int k = 0; k < kGroup; ++k)
+          if (!(keep >> k & 1u)) x[k] = -INFINITY;
+      }
+      if (!(any & kBiasBit)) {
+        store8(yg + i * kGroup, x);
+      } else {
+#pragma unroll
+        for (int k = 0; k < kGroup; ++k)
+          if (!(count[head + i * kGroup + k] & kBiasBit)) yg[i * kGroup + k] = Elem<out_t>::put(x[k]);
       }
     }
   }
-  __syncthreads();
-  const float rep = a.rep ? a.rep[b] : 1.f, freq = a.freq ? a.freq[b] : 0.f, pres = a.pres ? a.pres[b] : 0.f;
-  const in_t* z = static_cast<const in_t*>(a.z) + b * a.z_stride;
-  out_t* y = static_cast<out_t*>(a.y) + b * a.y_stride;
-  const uint32_t* mask = a.mask ? a.mask + b * a.mask_stride : nullptr;
-  int64_t bs = 0, be = 0;
-  if (a.b_ids) list_of(a.b_off, a.b_n, b, a.status, &bs, &be);
-  for (int32_t v = v0 + threadIdx.x; v < v1; v += kThreads) {
-    float x = penalised(Elem<in_t>::get(z[v]), count[v - v0], rep, freq, pres);
-    // a token's biases in the order of the list
-    for (int64_t j = bs; j < be; ++j)
-      if (a.b_ids[j] == v) x += a.b_val[j];
-    if (mask && !(mask[v >> 5] >> (v & 31) & 1u)) x = -INFINITY;
-    y[v] = Elem<out_t>::put(x);
+  // the few tokens before the first group and after the last
+  for (int32_t o = threadIdx.x; o < len - groups * kGroup; o += kLogitThreads) {
+    const int32_t at = o < head ? o : o + groups * kGroup;
+    const uint32_t c = kLists ? count[at] : 0;
+    if (!(c & kBiasBit)) y[at] = Elem<out_t>::put(allowed(v0 + at) ? penalty(Elem<in_t>::get(z[at]), c) : -INFINITY);
   }
-  for (int64_t j = bs + threadIdx.x; j < be; j += kThreads)
-    if (a.b_ids[j] < 0 || a.b_ids[j] >= a.V) report(a.status, kErrIndex);
+  // Each biased token by the thread of its first entry; its biases in list order.
+  for (int64_t j = bs + threadIdx.x; j < be; j += kLogitThreads) {
+    const int64_t v = a.b_ids[j];
+    if (v < v0 || v >= v0 + len) continue;
+    bool mine = true;
+    if (repeated)
+      for (int64_t i = bs; i < j && mine; ++i) mine = a.b_ids[i] != v;
+    if (!mine) continue;
+    float x = penalty(Elem<in_t>::get(z[v - v0]), count[v - v0]) + a.b_val[j];
+    if (repeated)
+      for (int64_t i = j + 1; i < be; ++i)
+        if (a.b_ids[i] == v) x += a.b_val[i];
+    y[v - v0] = Elem<out_t>::put(allowed((uint32_t)v) ? x : -INFINITY);
+  }
+}
+
+template <typename in_t, typename out_t>
+cudaError_t launch(int device, LogitsArgs& a, cudaStream_t s) {
+  void* args[] = {&a};
+  // Slices of 16384 tokens (64 KB of counts, three CTAs an SM); fewer rows take smaller
+  // ones, down to 2048, until the GPU has two CTAs an SM.
+  int log_slice = kMaxLogSlice;
+  while (log_slice > kMinLogSlice && (((int64_t)a.V * a.B) >> log_slice) < 2 * sm_count(device)) --log_slice;
+  a.log_slice = log_slice;
+  const dim3 grid((a.V + (1 << log_slice) - 1) >> log_slice, a.B);
+  if (!a.p_ids && !a.o_ids && !a.b_ids)
+    return launch_kernel(reinterpret_cast<const void*>(&k_logits<in_t, out_t, false>), grid, dim3(kLogitThreads), 0, s,
+                         args, false);
+  const void* fn = reinterpret_cast<const void*>(&k_logits<in_t, out_t, true>);
+  static bool ready[64];
+  const cudaError_t e = allow_smem(fn, ((1 << kMaxLogSlice) + 4) * 4, device, ready);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(fn, grid, dim3(kLogitThreads), ((1 << log_slice) + 4) * 4, s, args, false);
 }
 
 template <typename in_t>
-const void* logits_out(int out) {
+cudaError_t launch_out(int device, int out, LogitsArgs& a, cudaStream_t s) {
   switch (out) {
-    case EMB_F32: return reinterpret_cast<const void*>(&k_logits<in_t, float>);
-    case EMB_F16: return reinterpret_cast<const void*>(&k_logits<in_t, __half>);
-    default: return reinterpret_cast<const void*>(&k_logits<in_t, __nv_bfloat16>);
-  }
-}
-
-const void* logits_kernel(int in, int out) {
-  switch (in) {
-    case EMB_F32: return logits_out<float>(out);
-    case EMB_F16: return logits_out<__half>(out);
-    default: return logits_out<__nv_bfloat16>(out);
+    case EMB_F32: return launch<in_t, float>(device, a, s);
+    case EMB_F16: return launch<in_t, __half>(device, a, s);
+    default: return launch<in_t, __nv_bfloat16>(device, a, s);
   }
 }
 
 bool list_args_ok(const int64_t* ids, const int64_t* off, int64_t n) {
-  if (n < 0 || !aligned(ids, 8) || !aligned(off, 8)) return false;
+  if (n < 0 || n > INT32_MAX || !aligned(ids, 8) || !aligned(off, 8)) return false;
   return off || (!ids && n == 0);
 }
 
@@ -146,10 +332,13 @@ extern "C" emb_status emb_logits_process(
   if (logits == out && (logits_dtype != out_dtype || (B > 1 && logits_stride != out_stride))) return EMB_ERR_INVALID_ARG;
   LogitsArgs a{logits,     out,        logits_stride, out_stride,    B,        V,        prompt_ids, prompt_offsets,
                output_ids, output_offsets, bias_ids,  bias_offsets,  prompt_n, output_n, bias_n,     repetition,
-               frequency,  presence,   bias_values,   mask,          mask_stride, device_status};
+               frequency,  presence,   bias_values,   mask,          mask_stride, device_status, 0};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
   return on_device(device, [&] {
-    void* args[] = {&a};
-    return launch_kernel(logits_kernel(logits_dtype, out_dtype), dim3((V + kSlice - 1) / kSlice, B), dim3(kThreads), 0,
-                         static_cast<cudaStream_t>(stream), args, false);
+    switch (logits_dtype) {
+      case EMB_F32: return launch_out<float>(device, out_dtype, a, s);
+      case EMB_F16: return launch_out<__half>(device, out_dtype, a, s);
+      default: return launch_out<__nv_bfloat16>(device, out_dtype, a, s);
+    }
   });
 }

@@ -223,14 +223,11 @@ template <typename T, int kFormat, int kTok>
 cudaError_t launch(int device, const MatmulArgs& a, const uint8_t* x, const uint8_t* w, cudaStream_t s) {
   using S = Shape<kFormat, kTok>;
   const void* fn = reinterpret_cast<const void*>(&k_micro_matmul<T, kFormat, kTok>);
-  static bool ready[64] = {};  // idempotent: a race sets the same attribute twice
-  if (device >= 64 || !ready[device]) {
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
-    if (e != cudaSuccess) return e;
-    if (device < 64) ready[device] = true;
-  }
+  static bool ready[64];
+  cudaError_t e = allow_smem(fn, S::kSmem, device, ready);
+  if (e != cudaSuccess) return e;
   CUtensorMap wmap, xmap;
-  cudaError_t e = byte_matrix_map(&wmap, w, a.N, micro_row_bytes(a.K), kRows);
+  e = byte_matrix_map(&wmap, w, a.N, micro_row_bytes(a.K), kRows);
   if (e == cudaSuccess) e = byte_matrix_map(&xmap, x, a.M, micro_row_bytes(a.K), kTok);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (int64_t)((a.N + kRows - 1) / kRows) * ((a.M + kTok - 1) / kTok);
