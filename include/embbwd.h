@@ -391,7 +391,7 @@ emb_status emb_logits_process(int device, const void* logits, emb_dtype logits_d
                               void* stream);
 
 /* Distillation from a teacher's top logits. Row n of the student's logits z [N, V]
- * (V <= 2^20), tau = temperature > 0, p = softmax(z / tau), and the teacher's list of
+ * (N <= 2^23, V <= 2^20), tau = temperature > 0, p = softmax(z / tau), and the teacher's list of
  * K <= 1024 entries (teacher_ids int64, teacher_logits; row stride teacher_stride for
  * both), q_k = exp(t_k / tau - L):
  *   teacher_lse given (fp32[N], L = log of the teacher's whole sum of exp(t / tau)):

@@ -13,17 +13,31 @@
 // padding; a row without entries, or whose teacher has no mass (L = -infinity), has
 // loss 0 and gradient 0.
 //
-// Exponentials are base 2: p_v = 2^(z_v c - M c) / S with c = log2(e) / tau and M
-// the row's largest logit. Sums are held in fp32.
+// Exponentials are base 2: p_v = 2^((z_v - M) c) / S with c = log2(e) / tau and M the
+// row's largest logit. The difference comes first, so that rows masked with the type's
+// lowest value neither overflow nor lose their maximum. Sums are held in fp32.
+//
+// Forward and step: a cluster of CTAs holds a row in shared memory, brought there by bulk
+// copies: the row is read from HBM once and its gradient, computed in place, written once.
+// Its largest logit and sums are exchanged through distributed shared memory in one round.
+// Backward (its sums are known): blocks over pieces of the rows, one read and one write.
 #include <cmath>
 
-#include "vocab.cuh"
+#include "sm103.cuh"
 
 namespace embbwd {
 namespace {
 
 constexpr int kMaxList = 1024;   // longest teacher list
 constexpr int kRowThreads = 512;
+constexpr int kMaxCluster = 8;
+constexpr uint32_t kLoadBytes = 16384;              // of a bulk load with a barrier of its own
+constexpr uint32_t kSliceMost = 200 * 1024;         // bytes of a row that a CTA can hold
+constexpr uint32_t kSliceWanted = 66 * 1024;        // three CTAs an SM
+constexpr uint32_t kSliceLeast = 4 * 1024;
+constexpr int kLoads = kSliceMost / kLoadBytes + 1;
+constexpr int32_t kMaxDistillRows = 1 << 23;        // (rows x pieces of a row stay below 2^31)
+constexpr int kPiece = 8192;                        // elements of a block of the backward
 
 enum { kForward = 0, kBackward = 1, kStep = 2 };
 
@@ -47,11 +61,10 @@ struct DistillArgs {
 
 // The teacher's list of a row in shared memory.
 struct List {
-  int32_t id[kMaxList];  // -1: no entry
-  float q[kMaxList];
-  float z[kMaxList];     // the student's logit there
-  float scratch[36];
-  int repeated;          // some id occurs more than once
+  int32_t* id;   // [K], -1: no entry
+  float* q;      // [K]
+  float* z;      // [K] the student's logit there
+  int repeated;  // some id occurs more than once
 };
 
 // Is entry k the first with its id? Only looked for in rows where ids repeat.
@@ -70,10 +83,11 @@ __device__ __forceinline__ float q_of_token(const List& l, int k, int K) {
   return q;
 }
 
-// Reads the list; returns whether the row takes part. Sets l.q (given L, which is
-// found first if the caller has none), *L and *qsum.
+// Reads row n's list (the student's logits of the entries in [lo, hi)); returns whether the
+// row takes part. Sets l.q, *L and the sum of q. L is found here unless the caller knows it.
 template <typename T>
-__device__ bool read_list(const DistillArgs& a, int32_t n, List& l, float known_L, bool known, float* L, float* qsum) {
+__device__ __forceinline__ bool read_list(const DistillArgs& a, int32_t n, List& l, float* scratch, int32_t lo,
+                                          int32_t hi, float known_L, bool known, float* L, float* qsum) {
   const T* z = static_cast<const T*>(a.z) + n * a.z_stride;
   float big = -INFINITY, any = 0.f;
   for (int k = threadIdx.x; k < a.K; k += blockDim.x) {
@@ -83,21 +97,19 @@ __device__ bool read_list(const DistillArgs& a, int32_t n, List& l, float known_
     l.id[k] = ok ? (int32_t)id : -1;
     const float t = ok ? __fdiv_rn(load_as_float(a.t, a.t_dtype, n * a.t_stride + k), a.tau) : -INFINITY;
     l.q[k] = t;
-    l.z[k] = ok ? Elem<T>::get(z[id]) : 0.f;
+    l.z[k] = id >= lo && id < hi ? Elem<T>::get(z[id]) : 0.f;
     if (ok) any = 1.f;
     big = fmaxf(big, t);
   }
   *L = 0.f;
-  if (block_all<false>(any, l.scratch) == 0.f) return false;
+  if (block_all<false>(any, scratch) == 0.f) return false;
   *L = known_L;
   if (!known) {
-    big = block_all<true>(big, l.scratch);
+    big = block_all<true>(big, scratch);
     float s = 0.f;
     for (int k = threadIdx.x; k < a.K; k += blockDim.x) s += expf(l.q[k] - (isinf(big) ? 0.f : big));
-    s = block_all<false>(s, l.scratch);
-    *L = -INFINITY;
-    if (s == 0.f) return false;
-    *L = (isinf(big) ? 0.f : big) + logf(s);
+    s = block_all<false>(s, scratch);
+    *L = s == 0.f ? -INFINITY : (isinf(big) ? 0.f : big) + logf(s);
   }
   if (*L == -INFINITY) return false;
   float s = 0.f;
@@ -106,33 +118,55 @@ __device__ bool read_list(const DistillArgs& a, int32_t n, List& l, float known_
     l.q[k] = q;
     s += q;
   }
-  *qsum = block_all<false>(s, l.scratch);
+  *qsum = block_all<false>(s, scratch);
   return true;
 }
 
-// One block a row; the row is read once for its largest logit, once for its sums
-// and once for its gradient. A bitmap of the vocabulary marks the list.
-template <typename T, int kMode>
-__global__ void __launch_bounds__(kRowThreads) k_distill_row(DistillArgs a) {
+// The loss of a row (without tau^2) and the coefficient of its gradient off the list,
+// from M, S and the sum off the list. All threads of a block that read the whole list.
+__device__ __forceinline__ float loss_of(const DistillArgs& a, int32_t n, const List& l, float* scratch, float M,
+                                         float S, float L) {
+  const float logS = logf(S);
+  float ls = 0.f;
+  for (int k = threadIdx.x; k < a.K; k += blockDim.x)
+    if (l.q[k] > 0.f) {
+      const float logp = (l.z[k] - M) * (a.c2 * kLn2) - logS;
+      ls += l.q[k] * ((__fdiv_rn(load_as_float(a.t, a.t_dtype, n * a.t_stride + k), a.tau) - L) - logp);
+    } else if (!(l.q[k] == 0.f)) {
+      ls = NAN;
+    }
+  return block_all<false>(ls, scratch);
+}
+__device__ __forceinline__ float tail_of(float qsum, float rest, float S, float* coef) {
+  const float r = fmaxf(0.f, 1.f - qsum), u = rest / S;
+  *coef = r > 0.f ? 1.f - r / u : 1.f;
+  return r > 0.f ? r * (logf(r) - logf(u)) : 0.f;
+}
+
+// Rows too wide for a cluster: one block a row, which is read for its largest logit, for
+// its sums and for its gradient. A bitmap of the vocabulary marks the list.
+template <typename T, bool kGrad>
+__global__ void __launch_bounds__(kRowThreads) k_distill_wide(DistillArgs a) {
   extern __shared__ uint32_t on_list[];
   __shared__ List l;
+  __shared__ float scratch[33];
   const int32_t n = blockIdx.x;
+  const int32_t words = (a.V + 31) / 32;
   const T* z = static_cast<const T*>(a.z) + n * a.z_stride;
   T* dz = static_cast<T*>(a.dz) + n * a.dz_stride;
-  for (int i = threadIdx.x; i < (a.V + 31) / 32; i += kRowThreads) on_list[i] = 0;
-  if (threadIdx.x == 0) l.repeated = 0;
+  for (int i = threadIdx.x; i < words; i += kRowThreads) on_list[i] = 0;
+  if (threadIdx.x == 0) {
+    l.id = reinterpret_cast<int32_t*>(on_list + words), l.q = reinterpret_cast<float*>(l.id + a.K), l.z = l.q + a.K;
+    l.repeated = 0;
+  }
   __syncthreads();
-  float4 st = make_float4(0.f, 1.f, 0.f, 0.f);
-  if (kMode == kBackward) st = a.stats[n];
   float L = 0.f, qsum = 0.f;
-  const bool known = kMode == kBackward || a.lse != nullptr;
-  const float known_L = kMode == kBackward ? st.w : (a.lse ? a.lse[n] : 0.f);
-  if (!read_list<T>(a, n, l, known_L, known, &L, &qsum)) {
+  if (!read_list<T>(a, n, l, scratch, 0, a.V, a.lse ? a.lse[n] : 0.f, a.lse != nullptr, &L, &qsum)) {
     if (threadIdx.x == 0) {
-      if (kMode != kBackward) a.loss[n] = 0.f;
-      if (kMode == kForward) a.stats[n] = make_float4(0.f, 1.f, 0.f, L);
+      a.loss[n] = 0.f;
+      if (!kGrad) a.stats[n] = make_float4(0.f, 1.f, 0.f, L);
     }
-    if (kMode != kForward)
+    if (kGrad)
       for (int32_t v = threadIdx.x; v < a.V; v += kRowThreads) dz[v] = Elem<T>::put(0.f);
     return;
   }
@@ -141,72 +175,395 @@ __global__ void __launch_bounds__(kRowThreads) k_distill_row(DistillArgs a) {
       const uint32_t bit = 1u << (l.id[k] & 31);
       if (atomicOr(&on_list[l.id[k] >> 5], bit) & bit) l.repeated = 1;
     }
-  __syncthreads();
-  if (kMode != kBackward) {
-    float m = -INFINITY;
-    for (int32_t v = threadIdx.x; v < a.V; v += kRowThreads) m = fmaxf(m, Elem<T>::get(z[v]));
-    m = block_all<true>(m, l.scratch);
-    const float mc = m * a.c2;
-    float rest = 0.f, top = 0.f;
-    for (int32_t v = threadIdx.x; v < a.V; v += kRowThreads)
-      if (!(on_list[v >> 5] >> (v & 31) & 1u)) rest += exp2f(fmaf(Elem<T>::get(z[v]), a.c2, -mc));
-    rest = block_all<false>(rest, l.scratch);
-    for (int k = threadIdx.x; k < a.K; k += kRowThreads)
-      if (l.id[k] >= 0 && is_first(l, k)) top += exp2f(fmaf(l.z[k], a.c2, -mc));
-    top = block_all<false>(top, l.scratch);
-    const float S = rest + top, logS = logf(S);
-    float ls = 0.f;
-    for (int k = threadIdx.x; k < a.K; k += kRowThreads)
-      if (l.q[k] > 0.f) {
-        const float logp = fmaf(l.z[k], a.c2, -mc) * kLn2 - logS;
-        ls += l.q[k] * ((__fdiv_rn(load_as_float(a.t, a.t_dtype, n * a.t_stride + k), a.tau) - L) - logp);
-      } else if (!(l.q[k] == 0.f)) {
-        ls = NAN;
-      }
-    ls = block_all<false>(ls, l.scratch);
-    float coef = 1.f;
-    if (a.lse) {
-      const float r = fmaxf(0.f, 1.f - qsum), u = rest / S;
-      if (r > 0.f) {
-        ls += r * (logf(r) - logf(u));
-        coef = 1.f - r / u;
-      }
-    }
-    st = make_float4(m, S, coef, L);
-    if (threadIdx.x == 0) {
-      a.loss[n] = a.tau * a.tau * ls;
-      if (kMode == kForward) a.stats[n] = st;
-    }
+  float M = -INFINITY;
+  for (int32_t v = threadIdx.x; v < a.V; v += kRowThreads) M = fmaxf(M, Elem<T>::get(z[v]));
+  M = block_all<true>(M, scratch);
+  float rest = 0.f, top = 0.f;
+  for (int32_t v = threadIdx.x; v < a.V; v += kRowThreads)
+    if (!(on_list[v >> 5] >> (v & 31) & 1u)) rest += ex2((Elem<T>::get(z[v]) - M) * a.c2);
+  rest = block_all<false>(rest, scratch);
+  for (int k = threadIdx.x; k < a.K; k += kRowThreads)
+    if (l.id[k] >= 0 && is_first(l, k)) top += ex2((l.z[k] - M) * a.c2);
+  const float S = rest + block_all<false>(top, scratch);
+  float coef = 1.f, loss = loss_of(a, n, l, scratch, M, S, L);
+  if (a.lse) loss += tail_of(qsum, rest, S, &coef);
+  if (threadIdx.x == 0) {
+    a.loss[n] = a.tau * a.tau * loss;
+    if (!kGrad) a.stats[n] = make_float4(M, S, coef, L);
   }
-  if (kMode == kForward) return;
-  const float mc = st.x * a.c2, scale = (a.weight ? a.weight[n] : 1.f) * a.tau / st.y;
+  if (!kGrad) return;
+  const float scale = (a.weight ? a.weight[n] : 1.f) * a.tau;
   for (int32_t v = threadIdx.x; v < a.V; v += kRowThreads)
     if (!(on_list[v >> 5] >> (v & 31) & 1u))
-      dz[v] = Elem<T>::put(scale * st.z * exp2f(fmaf(Elem<T>::get(z[v]), a.c2, -mc)));
+      dz[v] = Elem<T>::put(scale * coef / S * ex2((Elem<T>::get(z[v]) - M) * a.c2));
   for (int k = threadIdx.x; k < a.K; k += kRowThreads)
     if (l.id[k] >= 0 && is_first(l, k))
-      dz[l.id[k]] = Elem<T>::put(scale * (exp2f(fmaf(l.z[k], a.c2, -mc)) - q_of_token(l, k, a.K) * st.y));
+      dz[l.id[k]] = Elem<T>::put(scale * (ex2((l.z[k] - M) * a.c2) / S - q_of_token(l, k, a.K)));
+}
+
+// 16 bytes of a row, as pairs of floats.
+template <typename T>
+struct Unit;
+template <>
+struct Unit<float> {
+  static constexpr int n = 4;
+  __device__ __forceinline__ static float max_of(uint4 v) {
+    return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+  }
+  __device__ __forceinline__ static void widen(uint4 v, F2 (&x)[2]) {
+    x[0] = F2::of(__uint_as_float(v.x), __uint_as_float(v.y));
+    x[1] = F2::of(__uint_as_float(v.z), __uint_as_float(v.w));
+  }
+  __device__ __forceinline__ static uint4 narrow(const float2 (&x)[2]) {
+    return make_uint4(__float_as_uint(x[0].x), __float_as_uint(x[0].y), __float_as_uint(x[1].x), __float_as_uint(x[1].y));
+  }
+};
+template <>
+struct Unit<__nv_bfloat16> {
+  static constexpr int n = 8;
+  __device__ __forceinline__ static float max_of(uint4 v) {
+    const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&v);
+    const float2 m = __bfloat1622float2(__hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3])));
+    return fmaxf(m.x, m.y);
+  }
+  __device__ __forceinline__ static void widen(uint4 v, F2 (&x)[4]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = F2::of(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  }
+  __device__ __forceinline__ static uint4 narrow(const float2 (&x)[4]) {
+    uint4 v;
+    __nv_bfloat162* p = reinterpret_cast<__nv_bfloat162*>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = __float22bfloat162_rn(x[i]);
+    return v;
+  }
+};
+template <>
+struct Unit<__half> {
+  static constexpr int n = 8;
+  __device__ __forceinline__ static float max_of(uint4 v) {
+    const __half2* p = reinterpret_cast<const __half2*>(&v);
+    const float2 m = __half22float2(__hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3])));
+    return fmaxf(m.x, m.y);
+  }
+  __device__ __forceinline__ static void widen(uint4 v, F2 (&x)[4]) {
+    const __half2* p = reinterpret_cast<const __half2*>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(p[i]);
+      x[i] = F2::of(f.x, f.y);
+    }
+  }
+  __device__ __forceinline__ static uint4 narrow(const float2 (&x)[4]) {
+    uint4 v;
+    __half2* p = reinterpret_cast<__half2*>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = __float22half2_rn(x[i]);
+    return v;
+  }
+};
+
+// Sizes of a cluster CTA's shared memory: the slice, its bitmap, the list.
+template <typename T>
+__host__ __device__ constexpr uint32_t slice_bytes(int32_t slice) {
+  return (uint32_t)(slice + Unit<T>::n) * sizeof(T);
+}
+__host__ __device__ constexpr uint32_t bitmap_bytes(int32_t slice) { return ((uint32_t)slice / 8 + 4 + 15) / 16 * 16; }
+template <typename T>
+constexpr size_t cluster_smem(int32_t slice, int K) {
+  return slice_bytes<T>(slice) + bitmap_bytes(slice) + (size_t)K * 12;
+}
+
+// A cluster a row, `slice` elements (a multiple of 64) a CTA. Element e of the slice lies
+// at position shift + e of the buffer, shift its place in 16 bytes of global memory, so that
+// whole 16-byte units are copied in bulk; the few elements beside them one by one.
+template <typename T, bool kGrad>
+__global__ void __launch_bounds__(kRowThreads, 3) k_distill_cluster(DistillArgs a, int32_t slice, int log_ctas) {
+  using U = Unit<T>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ List l;
+  __shared__ float scratch[33];
+  __shared__ float parts[3][kMaxCluster];  // of every CTA: largest logit, sums off and on the list
+  __shared__ uint64_t bars[kLoads];
+  __shared__ int abort;
+  const uint32_t ctas = 1u << log_ctas, rank = blockIdx.x & (ctas - 1);
+  const int32_t n = blockIdx.x >> log_ctas;
+  const int32_t r0 = min((int64_t)a.V, (int64_t)rank * slice), len = min(a.V - r0, slice);
+  const T* z = static_cast<const T*>(a.z) + n * a.z_stride + r0;
+  T* dz = static_cast<T*>(a.dz) + n * a.dz_stride + r0;
+  T* data = reinterpret_cast<T*>(smem);
+  uint4* units4 = reinterpret_cast<uint4*>(smem);
+  uint32_t* bitmap = reinterpret_cast<uint32_t*>(smem + slice_bytes<T>(slice));
+  const int32_t shift = (int32_t)(reinterpret_cast<uintptr_t>(z) / sizeof(T) % U::n);
+  const int32_t units = len ? (shift + len + U::n - 1) / U::n : 0;
+  const int32_t u0 = min(units, shift ? 1 : 0), u1 = max(u0, (shift + len) / U::n);  // units that are copied whole
+  const int32_t edge0 = min(len, u0 * U::n - shift), edge1 = max(edge0, min(len, u1 * U::n - shift));
+
+  for (int i = threadIdx.x; i < (int)bitmap_bytes(slice) / 4; i += kRowThreads) bitmap[i] = 0;
+  if (threadIdx.x == 0) {
+    l.id = reinterpret_cast<int32_t*>(smem + slice_bytes<T>(slice) + bitmap_bytes(slice));
+    l.q = reinterpret_cast<float*>(l.id + a.K), l.z = l.q + a.K;
+    l.repeated = 0;
+    abort = 0;
+    for (int i = 0; i < kLoads; ++i) mbar_init(smem_u32(&bars[i]), 1);
+    mbar_init_fence();
+  }
+  __syncthreads();
+  const int32_t hi = rank == 0 ? a.V : r0 + len;  // CTA 0 also finds the loss: it needs every entry's logit
+  float L = 0.f, qsum = 0.f;
+  const bool part =
+      read_list<T>(a, n, l, scratch, rank == 0 ? 0 : r0, hi, a.lse ? a.lse[n] : 0.f, a.lse != nullptr, &L, &qsum);
+  if (!part) {  // the same for the whole cluster
+    if (rank == 0 && threadIdx.x == 0) {
+      a.loss[n] = 0.f;
+      if (!kGrad) a.stats[n] = make_float4(0.f, 1.f, 0.f, L);
+    }
+    if constexpr (!kGrad) return;
+    for (int32_t u = threadIdx.x; u < units; u += kRowThreads) units4[u] = make_uint4(0, 0, 0, 0);
+  } else {
+    const uint32_t bytes = (uint32_t)(u1 - u0) * 16;
+    if (threadIdx.x == 0)
+      for (uint32_t i = 0; i * kLoadBytes < bytes; ++i) {
+        const uint32_t at = i * kLoadBytes, some = min(kLoadBytes, bytes - at);
+        mbar_expect(smem_u32(&bars[i]), some);
+        bulk_load(smem_u32(smem) + u0 * 16 + at, reinterpret_cast<const char*>(z + (u0 * U::n - shift)) + at, some,
+                  smem_u32(&bars[i]));
+      }
+    for (int32_t q = threadIdx.x; q < (u0 + units - u1) * U::n; q += kRowThreads) {  // the edge units
+      const int32_t p = q < u0 * U::n ? q : q + (u1 - u0) * U::n, e = p - shift;
+      data[p] = e >= 0 && e < len ? z[e] : Elem<T>::put(-INFINITY);
+    }
+    for (int k = threadIdx.x; k < a.K; k += kRowThreads) {
+      const int32_t e = l.id[k] - r0;
+      if (l.id[k] < 0 || e < 0 || e >= len) continue;
+      const uint32_t p = shift + e, bit = 1u << (p & 31);
+      if (atomicOr(&bitmap[p >> 5], bit) & bit) l.repeated = 1;
+    }
+    __syncthreads();
+    float m = -INFINITY;
+    for (int32_t u = threadIdx.x; u < units; u += kRowThreads) {
+      if (u >= u0 && u < u1) mbar_wait(smem_u32(&bars[(uint32_t)(u - u0) * 16 / kLoadBytes]), 0, &abort);
+      m = fmaxf(m, U::max_of(units4[u]));
+    }
+    m = block_all<true>(m, scratch);
+    const float ref = m == -INFINITY ? 0.f : m;
+    const F2 minus = F2::of(-ref, -ref), c2 = F2::of(a.c2, a.c2);
+    F2 sum = F2::of(0.f, 0.f);
+    const uint8_t* on_list = reinterpret_cast<const uint8_t*>(bitmap);
+#pragma unroll 2
+    for (int32_t u = threadIdx.x; u < units; u += kRowThreads) {
+      F2 x[U::n / 2];
+      U::widen(units4[u], x);
+      const uint32_t bits = U::n == 8 ? on_list[u] : on_list[u >> 1] >> (u & 1) * 4 & 15u;
+#pragma unroll
+      for (int i = 0; i < U::n / 2; ++i) {
+        const float2 y = ((x[i] + minus) * c2).get();
+        float2 e = make_float2(ex2(y.x), ex2(y.y));
+        if (bits >> 2 * i & 1u) e.x = 0.f;
+        if (bits >> 2 * i & 2u) e.y = 0.f;
+        sum = sum + F2::of(e.x, e.y);
+      }
+    }
+    float rest = sum.get().x + sum.get().y, top = 0.f;
+    for (int k = threadIdx.x; k < a.K; k += kRowThreads) {
+      const int32_t e = l.id[k] - r0;
+      if (l.id[k] >= 0 && e >= 0 && e < len && is_first(l, k)) top += ex2((l.z[k] - ref) * a.c2);
+    }
+    rest = block_all<false>(rest, scratch);
+    top = block_all<false>(top, scratch);
+    if (threadIdx.x < ctas) {
+      cluster_store(cluster_map(smem_u32(&parts[0][rank]), threadIdx.x), m);
+      cluster_store(cluster_map(smem_u32(&parts[1][rank]), threadIdx.x), rest);
+      cluster_store(cluster_map(smem_u32(&parts[2][rank]), threadIdx.x), top);
+    }
+    cluster_sync();
+    float M = -INFINITY, S = 0.f, off = 0.f;
+    for (uint32_t i = 0; i < ctas; ++i) M = fmaxf(M, parts[0][i]);
+    for (uint32_t i = 0; i < ctas; ++i) {
+      const float f = parts[0][i] == M ? 1.f : ex2((parts[0][i] - M) * a.c2);
+      off += parts[1][i] * f;
+      S += parts[2][i] * f;
+    }
+    S += off;
+    float coef = 1.f, tail = 0.f;
+    if (a.lse) tail = tail_of(qsum, off, S, &coef);
+    if (rank == 0) {
+      const float loss = loss_of(a, n, l, scratch, M, S, L) + tail;
+      if (threadIdx.x == 0) {
+        a.loss[n] = a.tau * a.tau * loss;
+        if (!kGrad) a.stats[n] = make_float4(M, S, coef, L);
+      }
+    }
+    if (!kGrad) {
+      if (threadIdx.x == 0 && abort) report(a.status, kErrTimeout);
+      return;
+    }
+    const float scale = (a.weight ? a.weight[n] : 1.f) * a.tau, g = scale * coef / S;
+    const F2 minus_M = F2::of(-M, -M), g2 = F2::of(g, g);
+#pragma unroll 2
+    for (int32_t u = threadIdx.x; u < units; u += kRowThreads) {
+      F2 x[U::n / 2];
+      U::widen(units4[u], x);
+      float2 e[U::n / 2];
+#pragma unroll
+      for (int i = 0; i < U::n / 2; ++i) {
+        const float2 y = ((x[i] + minus_M) * c2).get();
+        e[i] = (F2::of(ex2(y.x), ex2(y.y)) * g2).get();
+      }
+      units4[u] = U::narrow(e);
+    }
+    __syncthreads();
+    for (int k = threadIdx.x; k < a.K; k += kRowThreads) {
+      const int32_t e = l.id[k] - r0;
+      if (l.id[k] >= 0 && e >= 0 && e < len && is_first(l, k))
+        data[shift + e] = Elem<T>::put(scale * (ex2((l.z[k] - M) * a.c2) / S - q_of_token(l, k, a.K)));
+    }
+    if (threadIdx.x == 0 && abort) report(a.status, kErrTimeout);
+  }
+  proxy_fence();
+  __syncthreads();
+  if (reinterpret_cast<uintptr_t>(dz) / sizeof(T) % U::n != (uintptr_t)shift) {
+    for (int32_t e = threadIdx.x; e < len; e += kRowThreads) dz[e] = data[shift + e];
+    return;
+  }
+  for (int32_t q = threadIdx.x; q < edge0 + len - edge1; q += kRowThreads) {
+    const int32_t e = q < edge0 ? q : q - edge0 + edge1;
+    dz[e] = data[shift + e];
+  }
+  if (threadIdx.x == 0 && u1 > u0) {
+    bulk_store(dz + (u0 * U::n - shift), smem_u32(smem) + u0 * 16, (uint32_t)(u1 - u0) * 16);
+    bulk_commit();
+    bulk_wait_read();
+  }
+}
+
+// The gradient from the forward's sums: a block takes kPiece elements of a row.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_distill_backward(DistillArgs a, int32_t pieces) {
+  using U = Unit<T>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ uint32_t on_list[kPiece / 32];
+  __shared__ List l;
+  const int32_t n = blockIdx.x / pieces, r0 = (blockIdx.x - n * pieces) * kPiece, len = min(a.V - r0, kPiece);
+  const T* z = static_cast<const T*>(a.z) + n * a.z_stride + r0;
+  T* dz = static_cast<T*>(a.dz) + n * a.dz_stride + r0;
+  // units start `head` elements into the piece: stores 16-byte aligned, and loads too where both can be
+  const int32_t z_at = reinterpret_cast<uintptr_t>(z) / sizeof(T) % U::n;
+  const int32_t dz_at = reinterpret_cast<uintptr_t>(dz) / sizeof(T) % U::n;
+  const int32_t head = min(len, (U::n - dz_at) % U::n), units = (len - head) / U::n;
+  constexpr int kBatch = 4;
+  uint4 raw[kBatch];
+  const bool wide_loads = z_at == dz_at;
+  const uint4* zu = reinterpret_cast<const uint4*>(z + head);
+  auto load = [&](int k, int32_t u) {
+    if (wide_loads && u < units) raw[k] = zu[u];
+  };
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k) load(k, threadIdx.x + k * kThreads);
+  const float4 st = a.stats[n];
+  for (int i = threadIdx.x; i < kPiece / 32; i += kThreads) on_list[i] = 0;
+  if (threadIdx.x == 0) {
+    l.id = reinterpret_cast<int32_t*>(smem), l.q = reinterpret_cast<float*>(l.id + a.K), l.z = l.q + a.K;
+    l.repeated = 0;
+  }
+  __syncthreads();
+  int any = 0;
+  for (int k = threadIdx.x; k < a.K; k += kThreads) {
+    const int64_t id = a.ids[n * a.t_stride + k];
+    const bool ok = id >= 0 && id < a.V;
+    if (id < -1 || id >= a.V) report(a.status, kErrIndex);
+    any |= ok;
+    const int32_t e = ok ? (int32_t)id - r0 : -1;
+    const bool here = e >= 0 && e < len;
+    l.id[k] = here ? e : -1;
+    if (!here) continue;
+    l.q[k] = expf(__fdiv_rn(load_as_float(a.t, a.t_dtype, n * a.t_stride + k), a.tau) - st.w);
+    l.z[k] = Elem<T>::get(z[e]);
+    const uint32_t bit = 1u << (e & 31);
+    if (atomicOr(&on_list[e >> 5], bit) & bit) l.repeated = 1;
+  }
+  any = __syncthreads_or(any);
+  const bool part = any && st.w != -INFINITY;
+  const float scale = (a.weight ? a.weight[n] : 1.f) * a.tau, g = scale * st.z / st.y;
+  const F2 minus = F2::of(-st.x, -st.x), c2 = F2::of(a.c2, a.c2), g2 = F2::of(g, g);
+  for (int32_t i0 = threadIdx.x; i0 < units; i0 += kBatch * kThreads) {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int32_t u = i0 + k * kThreads;
+      if (u >= units) break;
+      if (!wide_loads) {
+        T* e = reinterpret_cast<T*>(&raw[k]);
+#pragma unroll
+        for (int i = 0; i < U::n; ++i) e[i] = z[head + u * U::n + i];
+      }
+      F2 x[U::n / 2];
+      U::widen(raw[k], x);
+      load(k, u + kBatch * kThreads);
+      float2 e[U::n / 2];
+#pragma unroll
+      for (int i = 0; i < U::n / 2; ++i) {
+        const float2 y = ((x[i] + minus) * c2).get();
+        e[i] = (F2::of(ex2(y.x), ex2(y.y)) * g2).get();
+      }
+      uint4 w = part ? U::narrow(e) : make_uint4(0, 0, 0, 0);
+      reinterpret_cast<uint4*>(dz + head)[u] = w;
+    }
+  }
+  for (int32_t o = threadIdx.x; o < len - units * U::n; o += kThreads) {
+    const int32_t e = o < head ? o : o + units * U::n;
+    dz[e] = Elem<T>::put(part ? g * ex2((Elem<T>::get(z[e]) - st.x) * a.c2) : 0.f);
+  }
+  if (!part) return;
+  __syncthreads();
+  for (int k = threadIdx.x; k < a.K; k += kThreads)
+    if (l.id[k] >= 0 && is_first(l, k))
+      dz[l.id[k]] = Elem<T>::put(scale * (ex2((l.z[k] - st.x) * a.c2) / st.y - q_of_token(l, k, a.K)));
 }
 
 template <typename T>
-const void* row_kernel(int mode) {
-  switch (mode) {
-    case kForward: return reinterpret_cast<const void*>(&k_distill_row<T, kForward>);
-    case kBackward: return reinterpret_cast<const void*>(&k_distill_row<T, kBackward>);
-    default: return reinterpret_cast<const void*>(&k_distill_row<T, kStep>);
+cudaError_t launch_rows(int device, bool grad, DistillArgs& a, cudaStream_t s) {
+  // The smallest cluster whose slices leave room for three CTAs an SM; more CTAs for few
+  // rows, while the GPU has not one each and slices stay above kSliceLeast.
+  int log_ctas = 0;
+  auto slice_of = [&] { return (int32_t)((((int64_t)a.V + (1 << log_ctas) - 1) / (1 << log_ctas) + 63) / 64 * 64); };
+  while ((1 << log_ctas) < kMaxCluster && slice_bytes<T>(slice_of()) > kSliceWanted) ++log_ctas;
+  while ((1 << log_ctas) < kMaxCluster && ((int64_t)a.N << log_ctas) < sm_count(device) &&
+         slice_bytes<T>(slice_of()) > kSliceLeast)
+    ++log_ctas;
+  int32_t slice = slice_of();
+  if (slice_bytes<T>(slice) <= kSliceMost && ((int64_t)a.N << log_ctas) <= INT32_MAX) {
+    const void* fn = grad ? reinterpret_cast<const void*>(&k_distill_cluster<T, true>)
+                          : reinterpret_cast<const void*>(&k_distill_cluster<T, false>);
+    static bool ready[2][64];
+    constexpr size_t most = kSliceMost + bitmap_bytes(kSliceMost / sizeof(T)) + kMaxList * 12;
+    static_assert(most < 225 * 1024, "");
+    const cudaError_t e = allow_smem(fn, most, device, ready[grad]);
+    if (e != cudaSuccess) return e;
+    void* args[] = {&a, &slice, &log_ctas};
+    return launch_clusters(fn, dim3((unsigned)a.N << log_ctas), dim3(kRowThreads), 1 << log_ctas,
+                           cluster_smem<T>(slice, a.K), s, args);
   }
+  const void* fn = grad ? reinterpret_cast<const void*>(&k_distill_wide<T, true>)
+                        : reinterpret_cast<const void*>(&k_distill_wide<T, false>);
+  static bool ready[2][64];
+  const cudaError_t e = allow_smem(fn, kMaxVocab / 8 + kMaxList * 12, device, ready[grad]);
+  if (e != cudaSuccess) return e;
+  void* args[] = {&a};
+  return launch_kernel(fn, dim3(a.N), dim3(kRowThreads), (size_t)((a.V + 31) / 32) * 4 + (size_t)a.K * 12, s, args, false);
 }
 
-const void* distill_kernel(int dtype, int mode) {
-  switch (dtype) {
-    case EMB_F32: return row_kernel<float>(mode);
-    case EMB_F16: return row_kernel<__half>(mode);
-    default: return row_kernel<__nv_bfloat16>(mode);
-  }
+template <typename T>
+cudaError_t launch_mode(int device, int mode, DistillArgs& a, cudaStream_t s) {
+  if (mode != kBackward) return launch_rows<T>(device, mode == kStep, a, s);
+  int32_t pieces = (a.V + kPiece - 1) / kPiece;
+  void* args[] = {&a, &pieces};
+  return launch_kernel(reinterpret_cast<const void*>(&k_distill_backward<T>), dim3((unsigned)a.N * pieces),
+                       dim3(kThreads), (size_t)a.K * 12, s, args, false);
 }
 
 emb_status distill(int device, int mode, int dtype, DistillArgs a, void* stream) {
-  if (device < 0 || a.N < 0 || a.V < 1 || a.V > kMaxVocab || a.K < 0 || a.K > kMaxList) return EMB_ERR_INVALID_ARG;
+  if (device < 0 || a.N < 0 || a.N > kMaxDistillRows || a.V < 1 || a.V > kMaxVocab || a.K < 0 || a.K > kMaxList) return EMB_ERR_INVALID_ARG;
   if (!dtype_ok(dtype) || !dtype_ok(a.t_dtype)) return EMB_ERR_INVALID_ARG;
   if (!(a.tau > 0.f) || !std::isfinite(a.tau)) return EMB_ERR_INVALID_ARG;
   if (!aligned(a.ids, 8) || !aligned(a.t, dtype_size(a.t_dtype)) || !aligned(a.lse, 4) || !aligned(a.weight, 4) ||
@@ -222,13 +579,13 @@ emb_status distill(int device, int mode, int dtype, DistillArgs a, void* stream)
     if (a.dz == a.z && a.N > 1 && a.dz_stride != a.z_stride) return EMB_ERR_INVALID_ARG;
   }
   a.c2 = (float)(1.4426950408889634 / (double)a.tau);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
   return on_device(device, [&] {
-    void* args[] = {&a};
-    const void* fn = distill_kernel(dtype, mode);
-    const size_t smem = (size_t)((a.V + 31) / 32) * 4;
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    return launch_kernel(fn, dim3(a.N), dim3(kRowThreads), smem, static_cast<cudaStream_t>(stream), args, false);
+    switch (dtype) {
+      case EMB_F32: return launch_mode<float>(device, mode, a, s);
+      case EMB_F16: return launch_mode<__half>(device, mode, a, s);
+      default: return launch_mode<__nv_bfloat16>(device, mode, a, s);
+    }
   });
 }
 

@@ -31,7 +31,6 @@ constexpr uint32_t kPromptBit = 0x80000000u, kBiasBit = 0x40000000u;  // of a to
 constexpr uint32_t kCountBits = kBiasBit - 1;
 constexpr int kMinLogSlice = 11, kMaxLogSlice = 14;  // tokens of a block, a power of two
 constexpr int kLogitThreads = 256, kLogitBlocks = 3;
-constexpr int kGroup = 8;                            // tokens of a thread and step
 constexpr int kBatch = 4;                            // steps whose loads are in flight together
 
 struct LogitsArgs {
@@ -71,37 +70,6 @@ struct Penalty {
     return n ? fmaf(-freq, (float)n, y) - pres : y;
   }
 };
-
-// Eight consecutive elements, 16-byte aligned: the load and the widening apart.
-template <typename T>
-struct Raw8 {
-  static constexpr int n = 16 / sizeof(T);
-  uint4 u[kGroup / n];
-  __device__ __forceinline__ void load(const T* p) {
-#pragma unroll
-    for (int i = 0; i < kGroup / n; ++i) u[i] = reinterpret_cast<const uint4*>(p)[i];
-  }
-  __device__ __forceinline__ void widen(float (&x)[kGroup]) const {
-#pragma unroll
-    for (int i = 0; i < kGroup / n; ++i) {
-      const T* e = reinterpret_cast<const T*>(&u[i]);
-#pragma unroll
-      for (int k = 0; k < n; ++k) x[i * n + k] = Elem<T>::get(e[k]);
-    }
-  }
-};
-template <typename T>
-__device__ __forceinline__ void store8(T* p, const float (&x)[kGroup]) {
-  constexpr int n = 16 / sizeof(T);
-#pragma unroll
-  for (int i = 0; i < kGroup / n; ++i) {
-    uint4 u;
-    T* e = reinterpret_cast<T*>(&u);
-#pragma unroll
-    for (int k = 0; k < n; ++k) e[k] = Elem<T>::put(x[i * n + k]);
-    reinterpret_cast<uint4*>(p)[i] = u;
-  }
-}
 
 // Counts a token in shared memory if off < len. Predicated: a warp's 32 ids rarely miss a
 // slice all together, and a branch around every atomic costs more than the atomic.

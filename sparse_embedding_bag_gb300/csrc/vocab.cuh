@@ -39,6 +39,39 @@ __device__ __forceinline__ float load_as_float(const void* p, int dtype, int64_t
   return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
 }
 
+constexpr int kGroup = 8;  // elements of a row that a thread takes together
+
+// Eight consecutive elements, 16-byte aligned: the load and the widening apart.
+template <typename T>
+struct Raw8 {
+  static constexpr int n = 16 / sizeof(T);
+  uint4 u[kGroup / n];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < kGroup / n; ++i) u[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+  __device__ __forceinline__ void widen(float (&x)[kGroup]) const {
+#pragma unroll
+    for (int i = 0; i < kGroup / n; ++i) {
+      const T* e = reinterpret_cast<const T*>(&u[i]);
+#pragma unroll
+      for (int k = 0; k < n; ++k) x[i * n + k] = Elem<T>::get(e[k]);
+    }
+  }
+};
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&x)[kGroup]) {
+  constexpr int n = 16 / sizeof(T);
+#pragma unroll
+  for (int i = 0; i < kGroup / n; ++i) {
+    uint4 u;
+    T* e = reinterpret_cast<T*>(&u);
+#pragma unroll
+    for (int k = 0; k < n; ++k) e[k] = Elem<T>::put(x[i * n + k]);
+    reinterpret_cast<uint4*>(p)[i] = u;
+  }
+}
+
 constexpr int32_t kMaxVocab = 1 << 20;  // widest row of logits
 
 constexpr float kLog2e = 1.4426950408889634f;
