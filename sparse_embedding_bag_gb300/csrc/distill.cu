@@ -83,26 +83,34 @@ __device__ __forceinline__ float q_of_token(const List& l, int k, int K) {
   return q;
 }
 
-// Reads row n's list (the student's logits of the entries in [lo, hi)); returns whether the
-// row takes part. Sets l.q, *L and the sum of q. L is found here unless the caller knows it.
-template <typename T>
-__device__ __forceinline__ bool read_list(const DistillArgs& a, int32_t n, List& l, float* scratch, int32_t lo,
-                                          int32_t hi, float known_L, bool known, float* L, float* qsum) {
-  const T* z = static_cast<const T*>(a.z) + n * a.z_stride;
-  float big = -INFINITY, any = 0.f;
+// Reads the ids of row n's list; returns whether there is any, to every thread.
+__device__ __forceinline__ bool read_ids(const DistillArgs& a, int32_t n, List& l) {
+  int any = 0;
   for (int k = threadIdx.x; k < a.K; k += blockDim.x) {
     const int64_t id = a.ids[n * a.t_stride + k];
     if (id < -1 || id >= a.V) report(a.status, kErrIndex);
     const bool ok = id >= 0 && id < a.V;
     l.id[k] = ok ? (int32_t)id : -1;
-    const float t = ok ? __fdiv_rn(load_as_float(a.t, a.t_dtype, n * a.t_stride + k), a.tau) : -INFINITY;
-    l.q[k] = t;
+    any |= ok;
+  }
+  return __syncthreads_or(any);
+}
+
+// The rest of the list (the student's logits of entries in [lo, hi)), each thread its own
+// entries; returns whether the row takes part. Sets l.q, *L and the sum of q. L is found
+// here unless the caller knows it.
+template <typename T>
+__device__ __forceinline__ bool read_list(const DistillArgs& a, int32_t n, List& l, float* scratch, int32_t lo,
+                                          int32_t hi, float known_L, bool known, float* L, float* qsum) {
+  const T* z = static_cast<const T*>(a.z) + n * a.z_stride;
+  float big = -INFINITY;
+  for (int k = threadIdx.x; k < a.K; k += blockDim.x) {
+    const int32_t id = l.id[k];
+    const float t = id >= 0 ? __fdiv_rn(load_as_float(a.t, a.t_dtype, n * a.t_stride + k), a.tau) : -INFINITY;
     l.z[k] = id >= lo && id < hi ? Elem<T>::get(z[id]) : 0.f;
-    if (ok) any = 1.f;
+    l.q[k] = t;
     big = fmaxf(big, t);
   }
-  *L = 0.f;
-  if (block_all<false>(any, scratch) == 0.f) return false;
   *L = known_L;
   if (!known) {
     big = block_all<true>(big, scratch);
@@ -149,7 +157,7 @@ template <typename T, bool kGrad>
 __global__ void __launch_bounds__(kRowThreads) k_distill_wide(DistillArgs a) {
   extern __shared__ uint32_t on_list[];
   __shared__ List l;
-  __shared__ float scratch[33];
+  __shared__ float scratch[64];
   const int32_t n = blockIdx.x;
   const int32_t words = (a.V + 31) / 32;
   const T* z = static_cast<const T*>(a.z) + n * a.z_stride;
@@ -161,7 +169,7 @@ __global__ void __launch_bounds__(kRowThreads) k_distill_wide(DistillArgs a) {
   }
   __syncthreads();
   float L = 0.f, qsum = 0.f;
-  if (!read_list<T>(a, n, l, scratch, 0, a.V, a.lse ? a.lse[n] : 0.f, a.lse != nullptr, &L, &qsum)) {
+  if (!read_ids(a, n, l) || !read_list<T>(a, n, l, scratch, 0, a.V, a.lse ? a.lse[n] : 0.f, a.lse != nullptr, &L, &qsum)) {
     if (threadIdx.x == 0) {
       a.loss[n] = 0.f;
       if (!kGrad) a.stats[n] = make_float4(0.f, 1.f, 0.f, L);
@@ -283,7 +291,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) k_distill_cluster(DistillArgs 
   using U = Unit<T>;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ List l;
-  __shared__ float scratch[33];
+  __shared__ float scratch[64];
   __shared__ float parts[3][kMaxCluster];  // of every CTA: largest logit, sums off and on the list
   __shared__ uint64_t bars[kLoads];
   __shared__ int abort;
@@ -310,26 +318,32 @@ __global__ void __launch_bounds__(kRowThreads, 3) k_distill_cluster(DistillArgs 
     mbar_init_fence();
   }
   __syncthreads();
-  const int32_t hi = rank == 0 ? a.V : r0 + len;  // CTA 0 also finds the loss: it needs every entry's logit
-  float L = 0.f, qsum = 0.f;
-  const bool part =
-      read_list<T>(a, n, l, scratch, rank == 0 ? 0 : r0, hi, a.lse ? a.lse[n] : 0.f, a.lse != nullptr, &L, &qsum);
+  // The row is asked for as soon as it is known to have a list.
+  const uint32_t bytes = (uint32_t)(u1 - u0) * 16;
+  bool part = read_ids(a, n, l);
+  if (part && threadIdx.x == 0)
+    for (uint32_t i = 0; i * kLoadBytes < bytes; ++i) {
+      const uint32_t at = i * kLoadBytes, some = min(kLoadBytes, bytes - at);
+      mbar_expect(smem_u32(&bars[i]), some);
+      bulk_load(smem_u32(smem) + u0 * 16 + at, reinterpret_cast<const char*>(z + (u0 * U::n - shift)) + at, some,
+                smem_u32(&bars[i]));
+    }
+  const int32_t lo = rank == 0 ? 0 : r0, hi = rank == 0 ? a.V : r0 + len;  // CTA 0 finds the loss: it needs every entry's logit
+  float L = 0.f, qsum = 0.f, M = -INFINITY, S = 0.f, tail = 0.f;
+  if (part) {
+    part = read_list<T>(a, n, l, scratch, lo, hi, a.lse ? a.lse[n] : 0.f, a.lse != nullptr, &L, &qsum);
+    if (!part)  // a teacher without mass: the copies under way end first
+      for (uint32_t i = 0; i * kLoadBytes < bytes; ++i) mbar_wait(smem_u32(&bars[i]), 0, &abort);
+  }
   if (!part) {  // the same for the whole cluster
     if (rank == 0 && threadIdx.x == 0) {
       a.loss[n] = 0.f;
       if (!kGrad) a.stats[n] = make_float4(0.f, 1.f, 0.f, L);
     }
     if constexpr (!kGrad) return;
+    __syncthreads();
     for (int32_t u = threadIdx.x; u < units; u += kRowThreads) units4[u] = make_uint4(0, 0, 0, 0);
   } else {
-    const uint32_t bytes = (uint32_t)(u1 - u0) * 16;
-    if (threadIdx.x == 0)
-      for (uint32_t i = 0; i * kLoadBytes < bytes; ++i) {
-        const uint32_t at = i * kLoadBytes, some = min(kLoadBytes, bytes - at);
-        mbar_expect(smem_u32(&bars[i]), some);
-        bulk_load(smem_u32(smem) + u0 * 16 + at, reinterpret_cast<const char*>(z + (u0 * U::n - shift)) + at, some,
-                  smem_u32(&bars[i]));
-      }
     for (int32_t q = threadIdx.x; q < (u0 + units - u1) * U::n; q += kRowThreads) {  // the edge units
       const int32_t p = q < u0 * U::n ? q : q + (u1 - u0) * U::n, e = p - shift;
       data[p] = e >= 0 && e < len ? z[e] : Elem<T>::put(-INFINITY);
@@ -370,15 +384,14 @@ __global__ void __launch_bounds__(kRowThreads, 3) k_distill_cluster(DistillArgs 
       const int32_t e = l.id[k] - r0;
       if (l.id[k] >= 0 && e >= 0 && e < len && is_first(l, k)) top += ex2((l.z[k] - ref) * a.c2);
     }
-    rest = block_all<false>(rest, scratch);
-    top = block_all<false>(top, scratch);
+    block_sums(rest, top, scratch);
     if (threadIdx.x < ctas) {
       cluster_store(cluster_map(smem_u32(&parts[0][rank]), threadIdx.x), m);
       cluster_store(cluster_map(smem_u32(&parts[1][rank]), threadIdx.x), rest);
       cluster_store(cluster_map(smem_u32(&parts[2][rank]), threadIdx.x), top);
     }
     cluster_sync();
-    float M = -INFINITY, S = 0.f, off = 0.f;
+    float off = 0.f;
     for (uint32_t i = 0; i < ctas; ++i) M = fmaxf(M, parts[0][i]);
     for (uint32_t i = 0; i < ctas; ++i) {
       const float f = parts[0][i] == M ? 1.f : ex2((parts[0][i] - M) * a.c2);
@@ -386,17 +399,16 @@ __global__ void __launch_bounds__(kRowThreads, 3) k_distill_cluster(DistillArgs 
       S += parts[2][i] * f;
     }
     S += off;
-    float coef = 1.f, tail = 0.f;
+    float coef = 1.f;
     if (a.lse) tail = tail_of(qsum, off, S, &coef);
-    if (rank == 0) {
+    if (threadIdx.x == 0 && abort) report(a.status, kErrTimeout);
+    if constexpr (!kGrad) {
+      if (rank != 0) return;
       const float loss = loss_of(a, n, l, scratch, M, S, L) + tail;
       if (threadIdx.x == 0) {
         a.loss[n] = a.tau * a.tau * loss;
-        if (!kGrad) a.stats[n] = make_float4(M, S, coef, L);
+        a.stats[n] = make_float4(M, S, coef, L);
       }
-    }
-    if (!kGrad) {
-      if (threadIdx.x == 0 && abort) report(a.status, kErrTimeout);
       return;
     }
     const float scale = (a.weight ? a.weight[n] : 1.f) * a.tau, g = scale * coef / S;
@@ -419,23 +431,26 @@ __global__ void __launch_bounds__(kRowThreads, 3) k_distill_cluster(DistillArgs 
       if (l.id[k] >= 0 && e >= 0 && e < len && is_first(l, k))
         data[shift + e] = Elem<T>::put(scale * (ex2((l.z[k] - M) * a.c2) / S - q_of_token(l, k, a.K)));
     }
-    if (threadIdx.x == 0 && abort) report(a.status, kErrTimeout);
   }
   proxy_fence();
   __syncthreads();
-  if (reinterpret_cast<uintptr_t>(dz) / sizeof(T) % U::n != (uintptr_t)shift) {
+  if (reinterpret_cast<uintptr_t>(dz) / sizeof(T) % U::n == (uintptr_t)shift) {
+    if (threadIdx.x == 0 && u1 > u0) {
+      bulk_store(dz + (u0 * U::n - shift), smem_u32(smem) + u0 * 16, bytes);
+      bulk_commit();
+    }
+    for (int32_t q = threadIdx.x; q < edge0 + len - edge1; q += kRowThreads) {
+      const int32_t e = q < edge0 ? q : q - edge0 + edge1;
+      dz[e] = data[shift + e];
+    }
+  } else {
     for (int32_t e = threadIdx.x; e < len; e += kRowThreads) dz[e] = data[shift + e];
-    return;
   }
-  for (int32_t q = threadIdx.x; q < edge0 + len - edge1; q += kRowThreads) {
-    const int32_t e = q < edge0 ? q : q - edge0 + edge1;
-    dz[e] = data[shift + e];
+  if (rank == 0 && part) {
+    const float loss = loss_of(a, n, l, scratch, M, S, L) + tail;
+    if (threadIdx.x == 0) a.loss[n] = a.tau * a.tau * loss;
   }
-  if (threadIdx.x == 0 && u1 > u0) {
-    bulk_store(dz + (u0 * U::n - shift), smem_u32(smem) + u0 * 16, (uint32_t)(u1 - u0) * 16);
-    bulk_commit();
-    bulk_wait_read();
-  }
+  if (threadIdx.x == 0) bulk_wait_read();
 }
 
 // The gradient from the forward's sums: a block takes kPiece elements of a row.

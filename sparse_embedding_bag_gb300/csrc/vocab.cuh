@@ -101,6 +101,17 @@ __device__ __forceinline__ float block_all(float v, float* scratch) {
   return kMax ? warp_max(v) : warp_sum(v);
 }
 
+// Both sums over a block; `scratch` holds 64 floats.
+__device__ __forceinline__ void block_sums(float& u, float& v, float* scratch) {
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  u = warp_sum(u), v = warp_sum(v);
+  __syncthreads();
+  if (lane == 0) scratch[warp] = u, scratch[32 + warp] = v;
+  __syncthreads();
+  u = warp_sum(lane < warps ? scratch[lane] : 0.f);
+  v = warp_sum(lane < warps ? scratch[32 + lane] : 0.f);
+}
+
 // ---- host side
 
 inline size_t dtype_size(int d) { return d == EMB_F32 ? 4 : 2; }
