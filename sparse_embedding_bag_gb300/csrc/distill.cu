@@ -13,14 +13,19 @@
 // padding; a row without entries, or whose teacher has no mass (L = -infinity), has
 // loss 0 and gradient 0.
 //
-// Exponentials are base 2: p_v = 2^((z_v - M) c) / S with c = log2(e) / tau and M the
-// row's largest logit. The difference comes first, so that rows masked with the type's
-// lowest value neither overflow nor lose their maximum. Sums are held in fp32.
+// Exponentials are base 2: 2^((z_v - ref) c), c = log2(e) / tau. Differences come first, so
+// that rows masked with the type's lowest value neither overflow nor lose their maximum.
+// Sums are held in fp32.
 //
-// Forward and step: a cluster of CTAs holds a row in shared memory, brought there by bulk
-// copies: the row is read from HBM once and its gradient, computed in place, written once.
-// Its largest logit and sums are exchanged through distributed shared memory in one round.
+// Forward and step: a cluster of CTAs takes a row, a part of it each. It streams its part
+// from HBM with a running reference (sums are rescaled when a value exceeds it by far, which
+// is rare after the first), the cluster exchanges largest logits and sums through
+// distributed shared memory in one round, and the step streams the part once more: it is
+// still in L2 (all rows under way are a third of it), so HBM sees one read and one write.
 // Backward (its sums are known): blocks over pieces of the rows, one read and one write.
+// Holding the rows in shared memory instead (bulk copies, three CTAs of 64 KB an SM) took
+// 474 us a step at 4096 x 128256 bf16, against 387: a CTA does nothing else while its
+// slice arrives, and reads it three times.
 #include <cmath>
 
 #include "sm103.cuh"
@@ -29,15 +34,12 @@ namespace embbwd {
 namespace {
 
 constexpr int kMaxList = 1024;   // longest teacher list
-constexpr int kRowThreads = 512;
 constexpr int kMaxCluster = 8;
-constexpr uint32_t kLoadBytes = 16384;              // of a bulk load with a barrier of its own
-constexpr uint32_t kSliceMost = 200 * 1024;         // bytes of a row that a CTA can hold
-constexpr uint32_t kSliceWanted = 66 * 1024;        // three CTAs an SM
-constexpr uint32_t kSliceLeast = 4 * 1024;
-constexpr int kLoads = kSliceMost / kLoadBytes + 1;
+constexpr int kRowBlocks = 5;                       // CTAs an SM of the row kernel
+constexpr int kBatch = 4;                           // 16-byte loads a thread has in flight
+constexpr int32_t kPartLeast = 2048;                // elements of a CTA's part of a row
 constexpr int32_t kMaxDistillRows = 1 << 23;        // (rows x pieces of a row stay below 2^31)
-constexpr int kPiece = 8192;                        // elements of a block of the backward
+constexpr int kPieceMost = 32768, kPieceLeast = 2048;      // elements of a block of the backward, a power of two
 
 enum { kForward = 0, kBackward = 1, kStep = 2 };
 
@@ -151,64 +153,6 @@ __device__ __forceinline__ float tail_of(float qsum, float rest, float S, float*
   return r > 0.f ? r * (logf(r) - logf(u)) : 0.f;
 }
 
-// Rows too wide for a cluster: one block a row, which is read for its largest logit, for
-// its sums and for its gradient. A bitmap of the vocabulary marks the list.
-template <typename T, bool kGrad>
-__global__ void __launch_bounds__(kRowThreads) k_distill_wide(DistillArgs a) {
-  extern __shared__ uint32_t on_list[];
-  __shared__ List l;
-  __shared__ float scratch[64];
-  const int32_t n = blockIdx.x;
-  const int32_t words = (a.V + 31) / 32;
-  const T* z = static_cast<const T*>(a.z) + n * a.z_stride;
-  T* dz = static_cast<T*>(a.dz) + n * a.dz_stride;
-  for (int i = threadIdx.x; i < words; i += kRowThreads) on_list[i] = 0;
-  if (threadIdx.x == 0) {
-    l.id = reinterpret_cast<int32_t*>(on_list + words), l.q = reinterpret_cast<float*>(l.id + a.K), l.z = l.q + a.K;
-    l.repeated = 0;
-  }
-  __syncthreads();
-  float L = 0.f, qsum = 0.f;
-  if (!read_ids(a, n, l) || !read_list<T>(a, n, l, scratch, 0, a.V, a.lse ? a.lse[n] : 0.f, a.lse != nullptr, &L, &qsum)) {
-    if (threadIdx.x == 0) {
-      a.loss[n] = 0.f;
-      if (!kGrad) a.stats[n] = make_float4(0.f, 1.f, 0.f, L);
-    }
-    if (kGrad)
-      for (int32_t v = threadIdx.x; v < a.V; v += kRowThreads) dz[v] = Elem<T>::put(0.f);
-    return;
-  }
-  for (int k = threadIdx.x; k < a.K; k += kRowThreads)
-    if (l.id[k] >= 0) {
-      const uint32_t bit = 1u << (l.id[k] & 31);
-      if (atomicOr(&on_list[l.id[k] >> 5], bit) & bit) l.repeated = 1;
-    }
-  float M = -INFINITY;
-  for (int32_t v = threadIdx.x; v < a.V; v += kRowThreads) M = fmaxf(M, Elem<T>::get(z[v]));
-  M = block_all<true>(M, scratch);
-  float rest = 0.f, top = 0.f;
-  for (int32_t v = threadIdx.x; v < a.V; v += kRowThreads)
-    if (!(on_list[v >> 5] >> (v & 31) & 1u)) rest += ex2((Elem<T>::get(z[v]) - M) * a.c2);
-  rest = block_all<false>(rest, scratch);
-  for (int k = threadIdx.x; k < a.K; k += kRowThreads)
-    if (l.id[k] >= 0 && is_first(l, k)) top += ex2((l.z[k] - M) * a.c2);
-  const float S = rest + block_all<false>(top, scratch);
-  float coef = 1.f, loss = loss_of(a, n, l, scratch, M, S, L);
-  if (a.lse) loss += tail_of(qsum, rest, S, &coef);
-  if (threadIdx.x == 0) {
-    a.loss[n] = a.tau * a.tau * loss;
-    if (!kGrad) a.stats[n] = make_float4(M, S, coef, L);
-  }
-  if (!kGrad) return;
-  const float scale = (a.weight ? a.weight[n] : 1.f) * a.tau;
-  for (int32_t v = threadIdx.x; v < a.V; v += kRowThreads)
-    if (!(on_list[v >> 5] >> (v & 31) & 1u))
-      dz[v] = Elem<T>::put(scale * coef / S * ex2((Elem<T>::get(z[v]) - M) * a.c2));
-  for (int k = threadIdx.x; k < a.K; k += kRowThreads)
-    if (l.id[k] >= 0 && is_first(l, k))
-      dz[l.id[k]] = Elem<T>::put(scale * (ex2((l.z[k] - M) * a.c2) / S - q_of_token(l, k, a.K)));
-}
-
 // 16 bytes of a row, as pairs of floats.
 template <typename T>
 struct Unit;
@@ -272,309 +216,318 @@ struct Unit<__half> {
   }
 };
 
-// Sizes of a cluster CTA's shared memory: the slice, its bitmap, the list.
+// How a part of a row at p is cut into 16-byte units: the first starts `head` elements into
+// it, at a multiple of 16 bytes.
 template <typename T>
-__host__ __device__ constexpr uint32_t slice_bytes(int32_t slice) {
-  return (uint32_t)(slice + Unit<T>::n) * sizeof(T);
-}
-__host__ __device__ constexpr uint32_t bitmap_bytes(int32_t slice) { return ((uint32_t)slice / 8 + 4 + 15) / 16 * 16; }
-template <typename T>
-constexpr size_t cluster_smem(int32_t slice, int K) {
-  return slice_bytes<T>(slice) + bitmap_bytes(slice) + (size_t)K * 12;
+struct Cut {
+  int32_t head, units;
+  __device__ __forceinline__ Cut(const T* p, int32_t len) {
+    constexpr int n = Unit<T>::n;
+    head = min(len, (int32_t)(-(reinterpret_cast<uintptr_t>(p) / sizeof(T)) % n)), units = (len - head) / n;
+  }
+  template <bool kWide>
+  __device__ __forceinline__ uint4 load(const T* z, int32_t u) const {
+    constexpr int n = Unit<T>::n;
+    if (kWide) return reinterpret_cast<const uint4*>(z + head)[u];
+    uint4 v;
+    T* e = reinterpret_cast<T*>(&v);
+#pragma unroll
+    for (int i = 0; i < n; ++i) e[i] = z[head + u * n + i];
+    return v;
+  }
+  // Elements beside the units, by number from 0 to len - units * n - 1.
+  __device__ __forceinline__ int32_t beside(int32_t o) const { return o < head ? o : o + units * Unit<T>::n; }
+};
+
+// 2^((x - ref) c) of a unit.
+template <int n>
+__device__ __forceinline__ void powers(const F2 (&x)[n], F2 minus_ref, F2 c2, F2 (&e)[n]) {
+#pragma unroll
+  for (int i = 0; i < n; ++i) {
+    const float2 y = ((x[i] + minus_ref) * c2).get();
+    e[i] = F2::of(ex2(y.x), ex2(y.y));
+  }
 }
 
-// A cluster a row, `slice` elements (a multiple of 64) a CTA. Element e of the slice lies
-// at position shift + e of the buffer, shift its place in 16 bytes of global memory, so that
-// whole 16-byte units are copied in bulk; the few elements beside them one by one.
-template <typename T, bool kGrad>
-__global__ void __launch_bounds__(kRowThreads, 3) k_distill_cluster(DistillArgs a, int32_t slice, int log_ctas) {
+// f(unit number, its elements as pairs, the largest of them) for a thread's units of a
+// part, kBatch loads ahead; `raw` holds the first.
+template <bool kWide, typename T, typename F>
+__device__ __forceinline__ void for_units(const T* z, const Cut<T>& cut, uint4 (&raw)[kBatch], F f) {
   using U = Unit<T>;
-  extern __shared__ __align__(16) uint8_t smem[];
+  for (int32_t u0 = threadIdx.x; u0 < cut.units; u0 += kBatch * kThreads) {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int32_t u = u0 + k * kThreads;
+      if (u >= cut.units) break;
+      const float most = U::max_of(raw[k]);
+      F2 x[U::n / 2];
+      U::widen(raw[k], x);
+      if (u + kBatch * kThreads < cut.units) raw[k] = cut.template load<kWide>(z, u + kBatch * kThreads);
+      f(u, x, most);
+    }
+  }
+}
+
+// A thread's first units of a part, asked for ahead of their use.
+template <bool kWide, typename T>
+__device__ __forceinline__ void load_first(const T* z, const Cut<T>& cut, uint4 (&raw)[kBatch]) {
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k)
+    if ((int)threadIdx.x + k * kThreads < cut.units)
+      raw[k] = cut.template load<kWide>(z, threadIdx.x + k * kThreads);
+}
+
+// The gradient of a part of a row off the list: g 2^(..), g = weight tau coefficient / S.
+template <bool kWide, typename T>
+__device__ __forceinline__ void store_gradient(const T* z, T* dz, int32_t len, const Cut<T>& cut, uint4 (&raw)[kBatch],
+                                               float c, float M, float g) {
+  using U = Unit<T>;
+  const F2 g2 = F2::of(g, g), c2 = F2::of(c, c), minus_M = F2::of(-M, -M);
+  uint4* out = reinterpret_cast<uint4*>(dz + cut.head);
+  for_units<kWide>(z, cut, raw, [&](int32_t u, const F2 (&x)[U::n / 2], float) {
+    F2 e[U::n / 2];
+    float2 w[U::n / 2];
+    powers(x, minus_M, c2, e);
+#pragma unroll
+    for (int i = 0; i < U::n / 2; ++i) w[i] = (e[i] * g2).get();
+    out[u] = U::narrow(w);
+  });
+  for (int32_t o = threadIdx.x; o < len - cut.units * U::n; o += kThreads) {
+    const int32_t e = cut.beside(o);
+    dz[e] = Elem<T>::put(g * ex2((Elem<T>::get(z[e]) - M) * c));
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store_zeros(T* dz, int32_t len, const Cut<T>& cut) {
+  for (int32_t u = threadIdx.x; u < cut.units; u += kThreads)
+    reinterpret_cast<uint4*>(dz + cut.head)[u] = make_uint4(0, 0, 0, 0);
+  for (int32_t o = threadIdx.x; o < len - cut.units * Unit<T>::n; o += kThreads) dz[cut.beside(o)] = Elem<T>::put(0.f);
+}
+
+// The listed tokens' gradient, stored over what store_gradient left there. Entries hold
+// elements of the part (-1: another part's).
+template <typename T>
+__device__ __forceinline__ void store_listed(const DistillArgs& a, T* dz, const List& l, float scale, float M,
+                                             float S) {
+  for (int k = threadIdx.x; k < a.K; k += kThreads)
+    if (l.id[k] >= 0 && is_first(l, k))
+      dz[l.id[k]] = Elem<T>::put(scale * (ex2((l.z[k] - M) * a.c2) / S - q_of_token(l, k, a.K)));
+}
+
+// Marks the list's tokens of [r0, r0 + len) in a bitmap: element e at bit e + first.
+__device__ __forceinline__ void mark_list(const DistillArgs& a, List& l, uint32_t* bitmap, int32_t r0, int32_t len,
+                                          int32_t first) {
+  for (int k = threadIdx.x; k < a.K; k += kThreads) {
+    const int32_t e = l.id[k] - r0, p = e + first;
+    if (l.id[k] < 0 || e < 0 || e >= len) continue;
+    if (atomicOr(&bitmap[p >> 5], 1u << (p & 31)) >> (p & 31) & 1u) l.repeated = 1;
+  }
+}
+
+// A cluster a row, `part_len` elements (a multiple of 64) a CTA.
+template <typename T, bool kGrad, bool kWide>
+__global__ void __launch_bounds__(kThreads, kRowBlocks) k_distill_rows(DistillArgs a, int32_t part_len, int log_ctas) {
+  using U = Unit<T>;
+  extern __shared__ __align__(16) uint32_t bitmap[];  // of the part; then the list
   __shared__ List l;
   __shared__ float scratch[64];
   __shared__ float parts[3][kMaxCluster];  // of every CTA: largest logit, sums off and on the list
-  __shared__ uint64_t bars[kLoads];
-  __shared__ int abort;
   const uint32_t ctas = 1u << log_ctas, rank = blockIdx.x & (ctas - 1);
   const int32_t n = blockIdx.x >> log_ctas;
-  const int32_t r0 = min((int64_t)a.V, (int64_t)rank * slice), len = min(a.V - r0, slice);
+  const int32_t r0 = min((int64_t)a.V, (int64_t)rank * part_len), len = min(a.V - r0, part_len);
   const T* z = static_cast<const T*>(a.z) + n * a.z_stride + r0;
-  T* dz = static_cast<T*>(a.dz) + n * a.dz_stride + r0;
-  T* data = reinterpret_cast<T*>(smem);
-  uint4* units4 = reinterpret_cast<uint4*>(smem);
-  uint32_t* bitmap = reinterpret_cast<uint32_t*>(smem + slice_bytes<T>(slice));
-  const int32_t shift = (int32_t)(reinterpret_cast<uintptr_t>(z) / sizeof(T) % U::n);
-  const int32_t units = len ? (shift + len + U::n - 1) / U::n : 0;
-  const int32_t u0 = min(units, shift ? 1 : 0), u1 = max(u0, (shift + len) / U::n);  // units that are copied whole
-  const int32_t edge0 = min(len, u0 * U::n - shift), edge1 = max(edge0, min(len, u1 * U::n - shift));
-
-  for (int i = threadIdx.x; i < (int)bitmap_bytes(slice) / 4; i += kRowThreads) bitmap[i] = 0;
+  T* dz = kGrad ? static_cast<T*>(a.dz) + n * a.dz_stride + r0 : nullptr;
+  const Cut<T> cut(z, len);  // the order of the sums goes by the logits' alignment alone
+  uint4 raw[kBatch];
+  load_first<true>(z, cut, raw);
+  const int32_t words = part_len / 32 + 1;  // units' bits start at bit 8: a byte or half of one each
+  const int32_t first = 8 - cut.head;
+  for (int32_t i = threadIdx.x; i < words; i += kThreads) bitmap[i] = 0;
   if (threadIdx.x == 0) {
-    l.id = reinterpret_cast<int32_t*>(smem + slice_bytes<T>(slice) + bitmap_bytes(slice));
-    l.q = reinterpret_cast<float*>(l.id + a.K), l.z = l.q + a.K;
+    l.id = reinterpret_cast<int32_t*>(bitmap + words), l.q = reinterpret_cast<float*>(l.id + a.K), l.z = l.q + a.K;
     l.repeated = 0;
-    abort = 0;
-    for (int i = 0; i < kLoads; ++i) mbar_init(smem_u32(&bars[i]), 1);
-    mbar_init_fence();
   }
   __syncthreads();
-  // The row is asked for as soon as it is known to have a list.
-  const uint32_t bytes = (uint32_t)(u1 - u0) * 16;
-  bool part = read_ids(a, n, l);
-  if (part && threadIdx.x == 0)
-    for (uint32_t i = 0; i * kLoadBytes < bytes; ++i) {
-      const uint32_t at = i * kLoadBytes, some = min(kLoadBytes, bytes - at);
-      mbar_expect(smem_u32(&bars[i]), some);
-      bulk_load(smem_u32(smem) + u0 * 16 + at, reinterpret_cast<const char*>(z + (u0 * U::n - shift)) + at, some,
-                smem_u32(&bars[i]));
-    }
-  const int32_t lo = rank == 0 ? 0 : r0, hi = rank == 0 ? a.V : r0 + len;  // CTA 0 finds the loss: it needs every entry's logit
-  float L = 0.f, qsum = 0.f, M = -INFINITY, S = 0.f, tail = 0.f;
-  if (part) {
-    part = read_list<T>(a, n, l, scratch, lo, hi, a.lse ? a.lse[n] : 0.f, a.lse != nullptr, &L, &qsum);
-    if (!part)  // a teacher without mass: the copies under way end first
-      for (uint32_t i = 0; i * kLoadBytes < bytes; ++i) mbar_wait(smem_u32(&bars[i]), 0, &abort);
-  }
+  // CTA 0 finds the loss: it needs the student's logit of every entry
+  const int32_t lo = rank == 0 ? 0 : r0, hi = rank == 0 ? a.V : r0 + len;
+  float L = 0.f, qsum = 0.f;
+  const bool part =
+      read_ids(a, n, l) &&
+      read_list<T>(a, n, l, scratch, lo, hi, a.lse ? a.lse[n] : 0.f, a.lse != nullptr, &L, &qsum);
   if (!part) {  // the same for the whole cluster
     if (rank == 0 && threadIdx.x == 0) {
       a.loss[n] = 0.f;
       if (!kGrad) a.stats[n] = make_float4(0.f, 1.f, 0.f, L);
     }
-    if constexpr (!kGrad) return;
-    __syncthreads();
-    for (int32_t u = threadIdx.x; u < units; u += kRowThreads) units4[u] = make_uint4(0, 0, 0, 0);
-  } else {
-    for (int32_t q = threadIdx.x; q < (u0 + units - u1) * U::n; q += kRowThreads) {  // the edge units
-      const int32_t p = q < u0 * U::n ? q : q + (u1 - u0) * U::n, e = p - shift;
-      data[p] = e >= 0 && e < len ? z[e] : Elem<T>::put(-INFINITY);
-    }
-    for (int k = threadIdx.x; k < a.K; k += kRowThreads) {
-      const int32_t e = l.id[k] - r0;
-      if (l.id[k] < 0 || e < 0 || e >= len) continue;
-      const uint32_t p = shift + e, bit = 1u << (p & 31);
-      if (atomicOr(&bitmap[p >> 5], bit) & bit) l.repeated = 1;
-    }
-    __syncthreads();
-    float m = -INFINITY;
-    for (int32_t u = threadIdx.x; u < units; u += kRowThreads) {
-      if (u >= u0 && u < u1) mbar_wait(smem_u32(&bars[(uint32_t)(u - u0) * 16 / kLoadBytes]), 0, &abort);
-      m = fmaxf(m, U::max_of(units4[u]));
-    }
-    m = block_all<true>(m, scratch);
-    const float ref = m == -INFINITY ? 0.f : m;
-    const F2 minus = F2::of(-ref, -ref), c2 = F2::of(a.c2, a.c2);
-    F2 sum = F2::of(0.f, 0.f);
-    const uint8_t* on_list = reinterpret_cast<const uint8_t*>(bitmap);
-#pragma unroll 2
-    for (int32_t u = threadIdx.x; u < units; u += kRowThreads) {
-      F2 x[U::n / 2];
-      U::widen(units4[u], x);
-      const uint32_t bits = U::n == 8 ? on_list[u] : on_list[u >> 1] >> (u & 1) * 4 & 15u;
-#pragma unroll
-      for (int i = 0; i < U::n / 2; ++i) {
-        const float2 y = ((x[i] + minus) * c2).get();
-        float2 e = make_float2(ex2(y.x), ex2(y.y));
-        if (bits >> 2 * i & 1u) e.x = 0.f;
-        if (bits >> 2 * i & 2u) e.y = 0.f;
-        sum = sum + F2::of(e.x, e.y);
-      }
-    }
-    float rest = sum.get().x + sum.get().y, top = 0.f;
-    for (int k = threadIdx.x; k < a.K; k += kRowThreads) {
-      const int32_t e = l.id[k] - r0;
-      if (l.id[k] >= 0 && e >= 0 && e < len && is_first(l, k)) top += ex2((l.z[k] - ref) * a.c2);
-    }
-    block_sums(rest, top, scratch);
-    if (threadIdx.x < ctas) {
-      cluster_store(cluster_map(smem_u32(&parts[0][rank]), threadIdx.x), m);
-      cluster_store(cluster_map(smem_u32(&parts[1][rank]), threadIdx.x), rest);
-      cluster_store(cluster_map(smem_u32(&parts[2][rank]), threadIdx.x), top);
-    }
-    cluster_sync();
-    float off = 0.f;
-    for (uint32_t i = 0; i < ctas; ++i) M = fmaxf(M, parts[0][i]);
-    for (uint32_t i = 0; i < ctas; ++i) {
-      const float f = parts[0][i] == M ? 1.f : ex2((parts[0][i] - M) * a.c2);
-      off += parts[1][i] * f;
-      S += parts[2][i] * f;
-    }
-    S += off;
-    float coef = 1.f;
-    if (a.lse) tail = tail_of(qsum, off, S, &coef);
-    if (threadIdx.x == 0 && abort) report(a.status, kErrTimeout);
-    if constexpr (!kGrad) {
-      if (rank != 0) return;
-      const float loss = loss_of(a, n, l, scratch, M, S, L) + tail;
-      if (threadIdx.x == 0) {
-        a.loss[n] = a.tau * a.tau * loss;
-        a.stats[n] = make_float4(M, S, coef, L);
-      }
-      return;
-    }
-    const float scale = (a.weight ? a.weight[n] : 1.f) * a.tau, g = scale * coef / S;
-    const F2 minus_M = F2::of(-M, -M), g2 = F2::of(g, g);
-#pragma unroll 2
-    for (int32_t u = threadIdx.x; u < units; u += kRowThreads) {
-      F2 x[U::n / 2];
-      U::widen(units4[u], x);
-      float2 e[U::n / 2];
-#pragma unroll
-      for (int i = 0; i < U::n / 2; ++i) {
-        const float2 y = ((x[i] + minus_M) * c2).get();
-        e[i] = (F2::of(ex2(y.x), ex2(y.y)) * g2).get();
-      }
-      units4[u] = U::narrow(e);
-    }
-    __syncthreads();
-    for (int k = threadIdx.x; k < a.K; k += kRowThreads) {
-      const int32_t e = l.id[k] - r0;
-      if (l.id[k] >= 0 && e >= 0 && e < len && is_first(l, k))
-        data[shift + e] = Elem<T>::put(scale * (ex2((l.z[k] - M) * a.c2) / S - q_of_token(l, k, a.K)));
-    }
+    if (kGrad) store_zeros(dz, len, Cut<T>(dz, len));
+    return;
   }
-  proxy_fence();
+  mark_list(a, l, bitmap, r0, len, first);
   __syncthreads();
-  if (reinterpret_cast<uintptr_t>(dz) / sizeof(T) % U::n == (uintptr_t)shift) {
-    if (threadIdx.x == 0 && u1 > u0) {
-      bulk_store(dz + (u0 * U::n - shift), smem_u32(smem) + u0 * 16, bytes);
-      bulk_commit();
+  // This thread's largest logit, and its sum off the list relative to a reference that is
+  // raised when a value exceeds it by a factor of 2^kSlack.
+  constexpr float kSlack = 16.f;
+  const float slack = kSlack / a.c2;
+  float m = -INFINITY, ref = -3.402823466e38f;
+  const F2 c2 = F2::of(a.c2, a.c2);
+  F2 sum = F2::of(0.f, 0.f);
+  auto raise = [&](float most) {
+    m = fmaxf(m, most);
+    if (most > ref + slack) {
+      const float f = ex2((ref - most) * a.c2);
+      sum = sum * F2::of(f, f);
+      ref = most;
     }
-    for (int32_t q = threadIdx.x; q < edge0 + len - edge1; q += kRowThreads) {
-      const int32_t e = q < edge0 ? q : q - edge0 + edge1;
-      dz[e] = data[shift + e];
+  };
+  const uint8_t* on_list = reinterpret_cast<const uint8_t*>(bitmap) + 1;
+  for_units<true>(z, cut, raw, [&](int32_t u, F2 (&x)[U::n / 2], float most) {
+    raise(most);
+    F2 e[U::n / 2];
+    const uint32_t bits = U::n == 8 ? on_list[u] : on_list[u >> 1] >> (u & 1) * 4 & 15u;
+    if (bits) {
+#pragma unroll
+      for (int i = 0; i < U::n / 2; ++i) {
+        const float2 y = x[i].get();
+        x[i] = F2::of(bits >> 2 * i & 1u ? -INFINITY : y.x, bits >> 2 * i & 2u ? -INFINITY : y.y);
+      }
     }
-  } else {
-    for (int32_t e = threadIdx.x; e < len; e += kRowThreads) dz[e] = data[shift + e];
+    powers(x, F2::of(-ref, -ref), c2, e);
+#pragma unroll
+    for (int i = 0; i < U::n / 2; ++i) sum = sum + e[i];
+  });
+  for (int32_t o = threadIdx.x; o < len - cut.units * U::n; o += kThreads) {
+    const int32_t e = cut.beside(o);
+    const float x = Elem<T>::get(z[e]);
+    raise(x);
+    if (!(bitmap[(e + first) >> 5] >> ((e + first) & 31) & 1u)) sum = sum + F2::of(ex2((x - ref) * a.c2), 0.f);
   }
-  if (rank == 0 && part) {
+  const Cut<T> again(kGrad ? dz : z, len);
+  if (kGrad) load_first<kWide>(z, again, raw);
+  // relative to the part's largest logit; with nothing but -infinity there is no sum
+  float M = block_all<true>(m, scratch);
+  float rest = sum.get().x + sum.get().y, top = 0.f;
+  const float base = M == -INFINITY ? 0.f : M;
+  rest *= ref == base ? 1.f : ex2((ref - base) * a.c2);
+  for (int k = threadIdx.x; k < a.K; k += kThreads) {
+    const int32_t e = l.id[k] - r0;
+    if (l.id[k] >= 0 && e >= 0 && e < len && is_first(l, k)) top += ex2((l.z[k] - base) * a.c2);
+  }
+  block_sums(rest, top, scratch);
+  if (threadIdx.x < ctas) {
+    cluster_store(cluster_map(smem_u32(&parts[0][rank]), threadIdx.x), M);
+    cluster_store(cluster_map(smem_u32(&parts[1][rank]), threadIdx.x), rest);
+    cluster_store(cluster_map(smem_u32(&parts[2][rank]), threadIdx.x), top);
+  }
+  cluster_sync();
+  float S = 0.f, off = 0.f;
+  for (uint32_t i = 0; i < ctas; ++i) M = fmaxf(M, parts[0][i]);
+  for (uint32_t i = 0; i < ctas; ++i) {
+    const float f = parts[0][i] == M ? 1.f : ex2((parts[0][i] - M) * a.c2);
+    off += parts[1][i] * f;
+    S += parts[2][i] * f;
+  }
+  S += off;
+  float coef = 1.f;
+  const float tail = a.lse ? tail_of(qsum, off, S, &coef) : 0.f;
+  const float scale = (a.weight ? a.weight[n] : 1.f) * a.tau;
+  if (kGrad) store_gradient<kWide>(z, dz, len, again, raw, a.c2, M, scale * coef / S);
+  if (rank == 0) {
     const float loss = loss_of(a, n, l, scratch, M, S, L) + tail;
-    if (threadIdx.x == 0) a.loss[n] = a.tau * a.tau * loss;
+    if (threadIdx.x == 0) {
+      a.loss[n] = a.tau * a.tau * loss;
+      if (!kGrad) a.stats[n] = make_float4(M, S, coef, L);
+    }
   }
-  if (threadIdx.x == 0) bulk_wait_read();
+  if (!kGrad) return;
+  __syncthreads();
+  for (int k = threadIdx.x; k < a.K; k += kThreads) {  // as elements of the part
+    const int32_t e = l.id[k] - r0;
+    l.id[k] = l.id[k] >= 0 && e >= 0 && e < len ? e : -1;
+  }
+  __syncthreads();
+  store_listed(a, dz, l, scale, M, S);
 }
 
-// The gradient from the forward's sums: a block takes kPiece elements of a row.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) k_distill_backward(DistillArgs a, int32_t pieces) {
-  using U = Unit<T>;
-  extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ uint32_t on_list[kPiece / 32];
+// The gradient from the forward's sums: a block takes `piece` elements of a row.
+template <typename T, bool kWide>
+__global__ void __launch_bounds__(kThreads, kRowBlocks) k_distill_backward(DistillArgs a, int32_t pieces, int32_t piece) {
+  extern __shared__ __align__(16) int32_t list[];
+  __shared__ uint32_t bitmap[kPieceMost / 32];
   __shared__ List l;
-  const int32_t n = blockIdx.x / pieces, r0 = (blockIdx.x - n * pieces) * kPiece, len = min(a.V - r0, kPiece);
+  const int32_t n = blockIdx.x / (uint32_t)pieces, r0 = (blockIdx.x - (uint32_t)n * pieces) * piece;
+  const int32_t len = min(a.V - r0, piece);
   const T* z = static_cast<const T*>(a.z) + n * a.z_stride + r0;
   T* dz = static_cast<T*>(a.dz) + n * a.dz_stride + r0;
-  // units start `head` elements into the piece: stores 16-byte aligned, and loads too where both can be
-  const int32_t z_at = reinterpret_cast<uintptr_t>(z) / sizeof(T) % U::n;
-  const int32_t dz_at = reinterpret_cast<uintptr_t>(dz) / sizeof(T) % U::n;
-  const int32_t head = min(len, (U::n - dz_at) % U::n), units = (len - head) / U::n;
-  constexpr int kBatch = 4;
+  const Cut<T> cut(dz, len);
   uint4 raw[kBatch];
-  const bool wide_loads = z_at == dz_at;
-  const uint4* zu = reinterpret_cast<const uint4*>(z + head);
-  auto load = [&](int k, int32_t u) {
-    if (wide_loads && u < units) raw[k] = zu[u];
-  };
-#pragma unroll
-  for (int k = 0; k < kBatch; ++k) load(k, threadIdx.x + k * kThreads);
+  load_first<kWide>(z, cut, raw);
   const float4 st = a.stats[n];
-  for (int i = threadIdx.x; i < kPiece / 32; i += kThreads) on_list[i] = 0;
-  if (threadIdx.x == 0) {
-    l.id = reinterpret_cast<int32_t*>(smem), l.q = reinterpret_cast<float*>(l.id + a.K), l.z = l.q + a.K;
-    l.repeated = 0;
-  }
+  for (int i = threadIdx.x; i < piece / 32; i += kThreads) bitmap[i] = 0;
+  if (threadIdx.x == 0)
+    l.id = list, l.q = reinterpret_cast<float*>(list + a.K), l.z = l.q + a.K, l.repeated = 0;
   __syncthreads();
-  int any = 0;
+  const bool part = read_ids(a, n, l) && st.w != -INFINITY;
   for (int k = threadIdx.x; k < a.K; k += kThreads) {
-    const int64_t id = a.ids[n * a.t_stride + k];
-    const bool ok = id >= 0 && id < a.V;
-    if (id < -1 || id >= a.V) report(a.status, kErrIndex);
-    any |= ok;
-    const int32_t e = ok ? (int32_t)id - r0 : -1;
-    const bool here = e >= 0 && e < len;
-    l.id[k] = here ? e : -1;
-    if (!here) continue;
+    const int32_t e = l.id[k] - r0;
+    if (l.id[k] < 0 || e < 0 || e >= len) {
+      l.id[k] = -1;
+      continue;
+    }
+    l.id[k] = e;
     l.q[k] = expf(__fdiv_rn(load_as_float(a.t, a.t_dtype, n * a.t_stride + k), a.tau) - st.w);
     l.z[k] = Elem<T>::get(z[e]);
-    const uint32_t bit = 1u << (e & 31);
-    if (atomicOr(&on_list[e >> 5], bit) & bit) l.repeated = 1;
+    if (atomicOr(&bitmap[e >> 5], 1u << (e & 31)) >> (e & 31) & 1u) l.repeated = 1;
   }
-  any = __syncthreads_or(any);
-  const bool part = any && st.w != -INFINITY;
-  const float scale = (a.weight ? a.weight[n] : 1.f) * a.tau, g = scale * st.z / st.y;
-  const F2 minus = F2::of(-st.x, -st.x), c2 = F2::of(a.c2, a.c2), g2 = F2::of(g, g);
-  for (int32_t i0 = threadIdx.x; i0 < units; i0 += kBatch * kThreads) {
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int32_t u = i0 + k * kThreads;
-      if (u >= units) break;
-      if (!wide_loads) {
-        T* e = reinterpret_cast<T*>(&raw[k]);
-#pragma unroll
-        for (int i = 0; i < U::n; ++i) e[i] = z[head + u * U::n + i];
-      }
-      F2 x[U::n / 2];
-      U::widen(raw[k], x);
-      load(k, u + kBatch * kThreads);
-      float2 e[U::n / 2];
-#pragma unroll
-      for (int i = 0; i < U::n / 2; ++i) {
-        const float2 y = ((x[i] + minus) * c2).get();
-        e[i] = (F2::of(ex2(y.x), ex2(y.y)) * g2).get();
-      }
-      uint4 w = part ? U::narrow(e) : make_uint4(0, 0, 0, 0);
-      reinterpret_cast<uint4*>(dz + head)[u] = w;
-    }
+  __syncthreads();  // in place, the listed logits are read before they are overwritten
+  const float scale = (a.weight ? a.weight[n] : 1.f) * a.tau;
+  if (!part) {
+    store_zeros(dz, len, cut);
+    return;
   }
-  for (int32_t o = threadIdx.x; o < len - units * U::n; o += kThreads) {
-    const int32_t e = o < head ? o : o + units * U::n;
-    dz[e] = Elem<T>::put(part ? g * ex2((Elem<T>::get(z[e]) - st.x) * a.c2) : 0.f);
-  }
-  if (!part) return;
+  store_gradient<kWide>(z, dz, len, cut, raw, a.c2, st.x, scale * st.z / st.y);
   __syncthreads();
-  for (int k = threadIdx.x; k < a.K; k += kThreads)
-    if (l.id[k] >= 0 && is_first(l, k))
-      dz[l.id[k]] = Elem<T>::put(scale * (ex2((l.z[k] - st.x) * a.c2) / st.y - q_of_token(l, k, a.K)));
+  store_listed(a, dz, l, scale, st.x, st.y);
+}
+
+// Do all rows of logits and gradient lie at the same places in 16 bytes? Then units that
+// store 16 bytes load 16 bytes.
+template <typename T>
+bool wide_loads(const DistillArgs& a) {
+  const uintptr_t z = reinterpret_cast<uintptr_t>(a.z), dz = reinterpret_cast<uintptr_t>(a.dz);
+  return (z - dz) % 16 == 0 && (a.N == 1 || (a.z_stride - a.dz_stride) % Unit<T>::n == 0);
 }
 
 template <typename T>
 cudaError_t launch_rows(int device, bool grad, DistillArgs& a, cudaStream_t s) {
-  // The smallest cluster whose slices leave room for three CTAs an SM; more CTAs for few
-  // rows, while the GPU has not one each and slices stay above kSliceLeast.
+  // Parts of at most 32768 elements (with a gradient, so that a part is still in L2 when it
+  // comes again) or 65536; smaller ones for few rows, while the GPU has not
+  // kRowBlocks CTAs an SM and parts stay above kPartLeast.
   int log_ctas = 0;
-  auto slice_of = [&] { return (int32_t)((((int64_t)a.V + (1 << log_ctas) - 1) / (1 << log_ctas) + 63) / 64 * 64); };
-  while ((1 << log_ctas) < kMaxCluster && slice_bytes<T>(slice_of()) > kSliceWanted) ++log_ctas;
-  while ((1 << log_ctas) < kMaxCluster && ((int64_t)a.N << log_ctas) < sm_count(device) &&
-         slice_bytes<T>(slice_of()) > kSliceLeast)
+  while ((1 << log_ctas) < kMaxCluster && (a.V >> log_ctas) > (grad ? 32768 : 65536)) ++log_ctas;
+  while ((1 << log_ctas) < kMaxCluster && ((int64_t)a.N << log_ctas) < kRowBlocks * sm_count(device) &&
+         (a.V >> log_ctas) > kPartLeast)
     ++log_ctas;
-  int32_t slice = slice_of();
-  if (slice_bytes<T>(slice) <= kSliceMost && ((int64_t)a.N << log_ctas) <= INT32_MAX) {
-    const void* fn = grad ? reinterpret_cast<const void*>(&k_distill_cluster<T, true>)
-                          : reinterpret_cast<const void*>(&k_distill_cluster<T, false>);
-    static bool ready[2][64];
-    constexpr size_t most = kSliceMost + bitmap_bytes(kSliceMost / sizeof(T)) + kMaxList * 12;
-    static_assert(most < 225 * 1024, "");
-    const cudaError_t e = allow_smem(fn, most, device, ready[grad]);
-    if (e != cudaSuccess) return e;
-    void* args[] = {&a, &slice, &log_ctas};
-    return launch_clusters(fn, dim3((unsigned)a.N << log_ctas), dim3(kRowThreads), 1 << log_ctas,
-                           cluster_smem<T>(slice, a.K), s, args);
-  }
-  const void* fn = grad ? reinterpret_cast<const void*>(&k_distill_wide<T, true>)
-                        : reinterpret_cast<const void*>(&k_distill_wide<T, false>);
-  static bool ready[2][64];
-  const cudaError_t e = allow_smem(fn, kMaxVocab / 8 + kMaxList * 12, device, ready[grad]);
-  if (e != cudaSuccess) return e;
-  void* args[] = {&a};
-  return launch_kernel(fn, dim3(a.N), dim3(kRowThreads), (size_t)((a.V + 31) / 32) * 4 + (size_t)a.K * 12, s, args, false);
+  int32_t part_len = ((a.V + (1 << log_ctas) - 1) >> log_ctas);
+  part_len = (part_len + 63) / 64 * 64;
+  const void* fn = !grad            ? reinterpret_cast<const void*>(&k_distill_rows<T, false, true>)
+                   : wide_loads<T>(a) ? reinterpret_cast<const void*>(&k_distill_rows<T, true, true>)
+                                      : reinterpret_cast<const void*>(&k_distill_rows<T, true, false>);
+  void* args[] = {&a, &part_len, &log_ctas};
+  return launch_clusters(fn, dim3((unsigned)a.N << log_ctas), dim3(kThreads), 1 << log_ctas,
+                         (size_t)part_len / 8 + 4 + (size_t)a.K * 12, s, args);
 }
 
 template <typename T>
 cudaError_t launch_mode(int device, int mode, DistillArgs& a, cudaStream_t s) {
   if (mode != kBackward) return launch_rows<T>(device, mode == kStep, a, s);
-  int32_t pieces = (a.V + kPiece - 1) / kPiece;
-  void* args[] = {&a, &pieces};
-  return launch_kernel(reinterpret_cast<const void*>(&k_distill_backward<T>), dim3((unsigned)a.N * pieces),
-                       dim3(kThreads), (size_t)a.K * 12, s, args, false);
+  // large pieces, so that the list is read by few blocks; smaller ones for few rows
+  int32_t piece = kPieceMost;
+  while (piece > kPieceLeast && (int64_t)a.N * ((a.V + piece - 1) / piece) < 2 * kRowBlocks * sm_count(device)) piece /= 2;
+  int32_t pieces = (a.V + piece - 1) / piece;
+  void* args[] = {&a, &pieces, &piece};
+  const void* fn = wide_loads<T>(a) ? reinterpret_cast<const void*>(&k_distill_backward<T, true>)
+                                    : reinterpret_cast<const void*>(&k_distill_backward<T, false>);
+  return launch_kernel(fn, dim3((unsigned)a.N * pieces), dim3(kThreads), (size_t)a.K * 12, s, args, false);
 }
 
 emb_status distill(int device, int mode, int dtype, DistillArgs a, void* stream) {
