@@ -1,10 +1,17 @@
 // Rows to microscaled 4-bit floating point, and back by row id.
+//
+// Both are bound by HBM traffic. A thread takes units of 8 elements, so that a warp's codes
+// are whole 128-byte lines and its 16-bit values whole 512-byte ones; a team of lanes (a
+// warp, or less for short rows) takes a piece of a row, kBatch loads of each lane in flight.
+// MEASURED
 #include <cmath>
 
 #include "micro.cuh"
 
 namespace embbwd {
 namespace {
+
+constexpr int kBatch = 4;  // units a thread has in flight
 
 struct QuantArgs {
   const void* x;
@@ -16,36 +23,66 @@ struct QuantArgs {
   uint8_t* scales;
 };
 
-// A thread takes one block of one row, in the padded range of the scale tiles.
+// Eight floats to eight codes.
+__device__ __forceinline__ uint32_t e2m1x8(const float (&x)[kGroup]) {
+  uint32_t r;
+  asm("{ .reg .b8 a, b, c, d;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+      "mov.b32 %0, {a, b, c, d}; }"
+      : "=r"(r)
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+  return r;
+}
+
+// Rows and blocks are taken up to whole scale tiles, whose padding is zero.
 template <typename T, int kFormat>
-__global__ void __launch_bounds__(kThreads) k_micro_quantize(QuantArgs a) {
-  constexpr int n = micro_block(kFormat);
-  const int32_t tiles = micro_tiles(a.K, kFormat);
-  const int64_t rows = (a.R + 127) / 128 * 128, total = rows * tiles * 4;
+__global__ void __launch_bounds__(kThreads) k_micro_quantize(QuantArgs a, int log_team) {
+  constexpr int n = micro_block(kFormat), lanes = n / kGroup;  // lanes of a block
+  const int32_t tiles = micro_tiles(a.K, kFormat), units = tiles * 4 * lanes;
   const int64_t row_bytes = micro_row_bytes(a.K);
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
-    const int64_t r = i / (tiles * 4);
-    const int32_t j = (int32_t)(i - r * (tiles * 4));
-    uint32_t byte = 0;
-    if (r < a.R && (int64_t)j * (n / 2) < row_bytes) {
-      const T* x = static_cast<const T*>(a.x) + r * a.x_stride;
-      float v[n], amax = 0.f;
-      bool nan = false;
+  const int32_t team = 1 << log_team, lane = threadIdx.x & 31;
+  const int64_t r = (int64_t)blockIdx.x * (kThreads >> log_team) + (threadIdx.x >> log_team);
+  const int32_t u0 = (int32_t)blockIdx.y * kBatch * team + (threadIdx.x & (team - 1));
+  const T* x = static_cast<const T*>(a.x) + r * a.x_stride;
+  const bool wide = reinterpret_cast<uintptr_t>(x) % 16 == 0;
+  Raw8<T> raw[kBatch];
 #pragma unroll
-      for (int e = 0; e < n; ++e) {
-        const int32_t k = j * n + e;
-        v[e] = k < a.K ? Elem<T>::get(x[k]) : 0.f;
-        amax = fmaxf(amax, fabsf(v[e]));
-        nan |= isnan(v[e]);
-      }
-      float f;
-      byte = micro_scale<kFormat>(nan ? NAN : amax, a.g, &f);
-      const bool bad = nan || isinf(amax);
+  for (int b = 0; b < kBatch; ++b) {
+    const int32_t k = (u0 + b * team) * kGroup;
+    if (r < a.R && wide && k + kGroup <= a.K) raw[b].load(x + k);
+  }
 #pragma unroll
-      for (int e = 0; e < n; e += 2)
-        a.codes[r * row_bytes + (j * n + e) / 2] = bad ? 0 : (uint8_t)e2m1x2(v[e] * f, v[e + 1] * f);
+  for (int b = 0; b < kBatch; ++b) {
+    const int32_t u = u0 + b * team, k = u * kGroup;
+    if (b > 0 && (int32_t)blockIdx.y * kBatch * team + b * team >= units) break;  // the same for the whole block
+    float v[kGroup];
+    if (r < a.R && wide && k + kGroup <= a.K) {
+      raw[b].widen(v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) v[i] = r < a.R && k + i < a.K ? Elem<T>::get(x[k + i]) : 0.f;
     }
-    a.scales[micro_scale_at(r, j, tiles)] = (uint8_t)byte;
+    // the largest magnitude by its bits: infinity is above all numbers, NaN above infinity
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) most = max(most, __float_as_uint(v[i]) & 0x7fffffffu);
+#pragma unroll
+    for (int o = 1; o < lanes; o *= 2) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+    float f;
+    const uint32_t byte = micro_scale<kFormat>(__uint_as_float(most), a.g, &f);
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) v[i] *= f;
+    const uint32_t codes = most >= 0x7f800000u ? 0u : e2m1x8(v);
+    if (r < a.R && (int64_t)u * 4 < row_bytes) *reinterpret_cast<uint32_t*>(a.codes + r * row_bytes + u * 4) = codes;
+    // four blocks' bytes make one word of the scale tile
+    uint32_t word = byte << ((lane / lanes & 3) * 8);
+    word |= __shfl_xor_sync(0xffffffffu, word, lanes);
+    word |= __shfl_xor_sync(0xffffffffu, word, 2 * lanes);
+    if (lane % (4 * lanes) == 0 && u < units && r < (a.R + 127) / 128 * 128)
+      *reinterpret_cast<uint32_t*>(a.scales + micro_scale_at(r, u / lanes, tiles)) = word;
   }
 }
 
@@ -62,29 +99,66 @@ struct LookupArgs {
   uint32_t* status;
 };
 
+template <int kFormat>
+__device__ __forceinline__ float micro_value(float v, float s, float g) {
+  return kFormat == kMicroMX ? v * s : __fmul_rn(v * s, g);
+}
+
+// Units start at the row's first 16-byte boundary of the output: stores are whole, and the
+// codes of a unit come from two words and two blocks where that is no multiple of 8.
 template <typename T, int kFormat>
-__global__ void __launch_bounds__(kThreads) k_micro_lookup(LookupArgs a) {
-  constexpr int n = micro_block(kFormat);
-  const int32_t tiles = micro_tiles(a.K, kFormat);
-  const int64_t row_bytes = micro_row_bytes(a.K);
-  const int32_t pairs = (a.K + 1) / 2;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < a.n * pairs; i += (int64_t)gridDim.x * kThreads) {
-    const int64_t row = i / pairs;
-    const int32_t k = (int32_t)(i - row * pairs) * 2;
-    const int64_t r = a.ids ? a.ids[row] : row;
-    float2 v = make_float2(0.f, 0.f);
-    if (r < 0 || r >= a.R) {
-      report(a.status, kErrIndex);
-    } else {
-      v = e2m1x2_values(a.codes[r * row_bytes + k / 2]);
-      const float s = micro_scale_value<kFormat>(a.scales[micro_scale_at(r, k / n, tiles)]);
-      v.x = kFormat == kMicroMX ? v.x * s : __fmul_rn(v.x * s, a.g);
-      v.y = kFormat == kMicroMX ? v.y * s : __fmul_rn(v.y * s, a.g);
-    }
-    T* out = static_cast<T*>(a.out) + row * a.out_stride + k;
-    out[0] = Elem<T>::put(v.x);
-    if (k + 1 < a.K) out[1] = Elem<T>::put(v.y);
+__global__ void __launch_bounds__(kThreads) k_micro_lookup(LookupArgs a, int log_team) {
+  constexpr int n = micro_block(kFormat), out_n = 16 / sizeof(T);
+  const int32_t team = 1 << log_team;
+  const int64_t row = (int64_t)blockIdx.x * (kThreads >> log_team) + (threadIdx.x >> log_team);
+  if (row >= a.n) return;
+  const int64_t r = a.ids ? a.ids[row] : row;
+  const bool ok = r >= 0 && r < a.R;
+  const int32_t tiles = micro_tiles(a.K, kFormat), first = threadIdx.x & (team - 1);
+  if (!ok && first == 0 && blockIdx.y == 0) report(a.status, kErrIndex);
+  const uint32_t* codes = reinterpret_cast<const uint32_t*>(a.codes + r * micro_row_bytes(a.K));
+  const uint8_t* scales = a.scales + micro_scale_at(r, 0, tiles);
+  auto scale_byte = [&](int32_t j) { return (uint32_t)__ldg(scales + (j >> 2) * 512 + (j & 3)); };
+  T* out = static_cast<T*>(a.out) + row * a.out_stride;
+  const int32_t head = min(a.K, (int32_t)(-(reinterpret_cast<uintptr_t>(out) / sizeof(T)) % out_n));
+  const int32_t units = (a.K - head) / kGroup;
+  const int32_t u0 = (int32_t)blockIdx.y * kBatch * team + first;
+  uint32_t word[kBatch], next[kBatch], byte[kBatch], byte2[kBatch];
+#pragma unroll
+  for (int b = 0; b < kBatch; ++b) {
+    const int32_t u = u0 + b * team, k = head + u * kGroup;
+    word[b] = next[b] = byte[b] = byte2[b] = 0;
+    if (!ok || u >= units) continue;
+    word[b] = __ldg(codes + k / 8);
+    byte[b] = scale_byte(k / n);
+    if (head) next[b] = __ldg(codes + (k + 7) / 8), byte2[b] = scale_byte((k + 7) / n);
   }
+#pragma unroll
+  for (int b = 0; b < kBatch; ++b) {
+    const int32_t u = u0 + b * team, k = head + u * kGroup;
+    if (u >= units) break;
+    const uint32_t w = __funnelshift_r(word[b], next[b], head * 4);
+    const float s = micro_scale_value<kFormat>(byte[b]), s2 = head ? micro_scale_value<kFormat>(byte2[b]) : s;
+    const int32_t same = n - k % n;  // elements of the unit in its first block
+    float x[kGroup];
+#pragma unroll
+    for (int i = 0; i < kGroup; i += 2) {
+      const float2 v = e2m1x2_values(w >> 4 * i & 0xffu);
+      x[i] = micro_value<kFormat>(v.x, i < same ? s : s2, a.g);
+      x[i + 1] = micro_value<kFormat>(v.y, i + 1 < same ? s : s2, a.g);
+    }
+    store8(out + k, x);
+  }
+  if (blockIdx.y == 0)
+    for (int32_t o = first; o < a.K - units * kGroup; o += team) {
+      const int32_t k = o < head ? o : o + units * kGroup;
+      float v = 0.f;
+      if (ok) {
+        const float2 pair = e2m1x2_values(codes[k / 8] >> (k & 6) * 4 & 0xffu);
+        v = micro_value<kFormat>(k & 1 ? pair.y : pair.x, micro_scale_value<kFormat>(scale_byte(k / n)), a.g);
+      }
+      out[k] = Elem<T>::put(v);
+    }
 }
 
 template <int kFormat>
@@ -105,9 +179,16 @@ const void* lookup_of(int dtype) {
   }
 }
 
-unsigned grid_for(int64_t items) {
-  const int64_t blocks = (items + kThreads - 1) / kThreads;
-  return (unsigned)(blocks < 152 * 8 ? blocks : 152 * 8);
+// Teams of the smallest power of two that holds a row's units, up to a warp, and at least
+// the lanes that make up a word of scales; blocks along y take pieces of a row.
+cudaError_t launch_teams(const void* fn, int64_t rows, int32_t units, int log_least, cudaStream_t s, void** args,
+                         int* log_team) {
+  *log_team = log_least;
+  while (*log_team < 5 && (1 << *log_team) < units) ++*log_team;
+  const int64_t per_block = kThreads >> *log_team;
+  const int32_t piece = kBatch << *log_team;
+  return launch_kernel(fn, dim3((unsigned)((rows + per_block - 1) / per_block), (units + piece - 1) / piece),
+                       dim3(kThreads), 0, s, args, false);
 }
 
 }  // namespace
@@ -127,10 +208,12 @@ extern "C" emb_status emb_micro_quantize(int device, const void* x, emb_dtype x_
     return EMB_ERR_INVALID_ARG;
   QuantArgs a{x, x_stride, R, K, tensor_scale, codes, scales};
   return on_device(device, [&] {
-    void* args[] = {&a};
-    const void* fn = format == EMB_MICRO_MX ? quantize_of<kMicroMX>(x_dtype) : quantize_of<kMicroNV>(x_dtype);
-    const int64_t items = (R + 127) / 128 * 128 * micro_tiles(K, format) * 4;
-    return launch_kernel(fn, dim3(grid_for(items)), dim3(kThreads), 0, static_cast<cudaStream_t>(stream), args, false);
+    int log_team;
+    void* args[] = {&a, &log_team};
+    const bool mx = format == EMB_MICRO_MX;
+    return launch_teams(mx ? quantize_of<kMicroMX>(x_dtype) : quantize_of<kMicroNV>(x_dtype), (R + 127) / 128 * 128,
+                        micro_tiles(K, format) * 4 * micro_block(format) / kGroup, mx ? 4 : 3,
+                        static_cast<cudaStream_t>(stream), args, &log_team);
   });
 }
 
@@ -148,9 +231,9 @@ extern "C" emb_status emb_micro_lookup(int device, const uint8_t* codes, const u
     return EMB_ERR_INVALID_ARG;
   LookupArgs a{codes, scales, R, K, tensor_scale, ids, n, out, out_stride, device_status};
   return on_device(device, [&] {
-    void* args[] = {&a};
-    const void* fn = format == EMB_MICRO_MX ? lookup_of<kMicroMX>(out_dtype) : lookup_of<kMicroNV>(out_dtype);
-    return launch_kernel(fn, dim3(grid_for(n * ((K + 1) / 2))), dim3(kThreads), 0, static_cast<cudaStream_t>(stream),
-                         args, false);
+    int log_team;
+    void* args[] = {&a, &log_team};
+    return launch_teams(format == EMB_MICRO_MX ? lookup_of<kMicroMX>(out_dtype) : lookup_of<kMicroNV>(out_dtype), n,
+                        (K + kGroup - 1) / kGroup, 0, static_cast<cudaStream_t>(stream), args, &log_team);
   });
 }

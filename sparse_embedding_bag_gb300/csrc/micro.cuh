@@ -42,12 +42,6 @@ __host__ __device__ inline int64_t micro_scale_at(int64_t r, int32_t j, int32_t 
   return ((r >> 7) * tiles + (j >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (j & 3);
 }
 
-// Two floats to two codes (round to nearest even, saturating): `lo` in bits 0-3.
-__device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
-  uint32_t r;
-  asm("{ .reg .b8 t; cvt.rn.satfinite.e2m1x2.f32 t, %1, %2; cvt.u32.u8 %0, t; }" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 // Two codes (bits 0-7) to their values.
 __device__ __forceinline__ float2 e2m1x2_values(uint32_t codes) {
   uint32_t h;
