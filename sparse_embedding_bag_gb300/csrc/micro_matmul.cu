@@ -50,9 +50,9 @@ struct Shape {
   static constexpr uint32_t kStages = (kSmemMost - 2048) / kStageAligned < 12 ? (kSmemMost - 2048) / kStageAligned : 12;
   static constexpr uint32_t kSmem = kStages * kStageAligned + 2048;
   static constexpr uint32_t kSfCols = kTiles * 4 * (1 + kTokTiles);
-  static constexpr uint32_t kSfA = kTmemCols - kSfCols, kSfB = kSfA + kTiles * 4;
+  static constexpr uint32_t kSf = kTmemCols - kSfCols;  // a stage's scales: the table's, then the tokens'
   // The second accumulator, and how many columns it shares with the first.
-  static constexpr uint32_t kAcc1 = 2 * kTok <= kSfA ? kTok : kSfA - kTok;
+  static constexpr uint32_t kAcc1 = 2 * kTok <= kSf ? kTok : kSf - kTok;
   static constexpr uint32_t kShared = kTok - kAcc1;
   static_assert(kShared % 8 == 0 && kStages >= 2, "");
 };
@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kMatmulThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ Control ctl;
   const uint32_t stages = (smem_u32(smem_raw) + 1023) & ~1023u;
-  const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   volatile int* abort = &ctl.abort;
   const int32_t w_tiles = (a.N + kRows - 1) / kRows, x_tiles = (a.M + kTok - 1) / kTok;
   const int64_t tiles = (int64_t)w_tiles * x_tiles;
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kMatmulThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = ctl.tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl.tmem, 0);
 
   if (warp == 4 && lane == 0) {
     uint32_t s = 0, round = 0;
@@ -143,45 +143,54 @@ __global__ void __launch_bounds__(kMatmulThreads, 1)
     // A : table codes, B : token codes, both E2M1, fp32 sums (bits 7, 10); N / 8 (17); E8M0 scales (23); M / 128 (27)
     constexpr uint32_t idesc0 = 1u << 7 | 1u << 10 | (uint32_t)(kTok / 8) << 17 |
                                 (kFormat == kMicroMX ? 1u << 23 : 0u) | (uint32_t)(kRows / 128) << 27;
-    if (lane == 0) {
-      uint32_t s = 0, round = 0;
-      bool ok = true;
-      uint32_t j = 0;
-      for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++j) {
-        constexpr uint32_t lag = S::kShared ? 1 : 2;  // the tile whose columns this one takes over
-        if (j >= lag && !mbar_wait(smem_u32(&ctl.acc_empty[(j - lag) & 1]), ((j - lag) >> 1) & 1, abort)) break;
+    // The whole warp walks the stages, so that addresses and descriptors stay in uniform
+    // registers; one lane issues. This warp paces the kernel: a stage is unrolled, with
+    // constant offsets.
+    const bool leader = elect_one();
+    const uint32_t full0 = smem_u32(&ctl.full[0]), empty0 = smem_u32(&ctl.empty[0]);
+    const uint32_t sfa = tmem + S::kSf, sfb = sfa + S::kTiles * 4;
+    constexpr uint32_t kBlock = S::kStageAligned >> 4;  // of a stage, in a descriptor's units
+    const uint64_t a_desc0 = operand_desc(stages), sf_desc0 = scales_desc(stages + S::kA + S::kB);
+    uint32_t s = 0, parity = 0, j = 0;
+    bool ok = true;
+    for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++j) {
+      constexpr uint32_t lag = S::kShared ? 1 : 2;  // the tile whose columns this one takes over
+      if (j >= lag && !mbar_wait(smem_u32(&ctl.acc_empty[(j - lag) & 1]), ((j - lag) >> 1) & 1, abort)) break;
+      const uint32_t d = tmem + ((j & 1) ? S::kAcc1 : 0);
+      for (int32_t k = 0; k < k_stages; ++k) {
+        if (!mbar_wait(full0 + s * 8, parity, abort)) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
-        const uint32_t d = tmem + ((j & 1) ? S::kAcc1 : 0);
-        for (int32_t k = 0; k < k_stages; ++k) {
-          if (!mbar_wait(smem_u32(&ctl.full[s]), round & 1, abort)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t base = stages + s * S::kStageAligned, sf = base + S::kA + S::kB;
-          const int32_t steps = min(kDepth / kStep, (a.K - k * kDepth + kStep - 1) / kStep);
-          const uint32_t used = min((int32_t)S::kTiles, sf_tiles - k * (int32_t)S::kTiles);
-          for (uint32_t i = 0; i < used; ++i) {
-            tc_copy_scales(tmem + S::kSfA + i * 4, scales_desc(sf + i * 512));
+        const uint64_t a_desc = a_desc0 + s * kBlock, b_desc = a_desc + (S::kA >> 4), sf_desc = sf_desc0 + s * kBlock;
+        const int32_t used = sf_tiles - k * (int32_t)S::kTiles, steps = (a.K - k * kDepth + kStep - 1) / kStep;
+        if (leader) {
+#pragma unroll
+          for (int i = 0; i < (int)S::kTiles; ++i) {
+            if (i >= used) break;
+            tc_copy_scales(sfa + i * 4, sf_desc + i * 32);
+#pragma unroll
             for (uint32_t q = 0; q < S::kTokTiles; ++q)
-              tc_copy_scales(tmem + S::kSfB + (i * S::kTokTiles + q) * 4,
-                             scales_desc(sf + S::kSA + (q * S::kTiles + i) * 512));
+              tc_copy_scales(sfb + (i * S::kTokTiles + q) * 4, sf_desc + (S::kSA >> 4) + (q * S::kTiles + i) * 32);
           }
-          for (int32_t e = 0; e < steps; ++e) {
+#pragma unroll
+          for (int e = 0; e < kDepth / kStep; ++e) {
+            if (e >= steps) break;
             // MX: a scale tile serves two steps, its bytes 0-1 and 2-3; NV: a tile a step
             const uint32_t i = kFormat == kMicroMX ? e >> 1 : e;
             const uint32_t id = kFormat == kMicroMX ? (e & 1) * 2 : 0;
-            tc_mma_f4<kFormat == kMicroMX>(d, operand_desc(base + e * 32), operand_desc(base + S::kA + e * 32),
-                                           idesc0 | id << 29 | id << 4, tmem + S::kSfA + i * 4,
-                                           tmem + S::kSfB + i * S::kTokTiles * 4, k | e);
+            tc_mma_f4<kFormat == kMicroMX>(d, a_desc + e * 2, b_desc + e * 2, idesc0 | id << 29 | id << 4, sfa + i * 4,
+                                           sfb + i * S::kTokTiles * 4, e > 0 || k > 0);
           }
-          tc_commit(smem_u32(&ctl.empty[s]));
-          if (++s == S::kStages) s = 0, ++round;
+          tc_commit(empty0 + s * 8);
+          if (k + 1 == k_stages) tc_commit(smem_u32(&ctl.acc_full[j & 1]));
         }
-        if (ok) tc_commit(smem_u32(&ctl.acc_full[j & 1]));
+        __syncwarp();
+        if (++s == S::kStages) s = 0, parity ^= 1;
       }
-      tc_commit(smem_u32(&ctl.done));
     }
+    if (leader) tc_commit(smem_u32(&ctl.done));
   } else if (warp < 4) {
     uint32_t j = 0;
     for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, ++j) {
