@@ -52,6 +52,8 @@ class EmbError(RuntimeError):
 def load(path: str = LIB_PATH):
     """Loads the library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
