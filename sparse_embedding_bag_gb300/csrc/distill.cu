@@ -514,7 +514,7 @@ cudaError_t launch_rows(int device, bool grad, DistillArgs& a, cudaStream_t s) {
                                       : reinterpret_cast<const void*>(&k_distill_rows<T, true, false>);
   void* args[] = {&a, &part_len, &log_ctas};
   return launch_clusters(fn, dim3((unsigned)a.N << log_ctas), dim3(kThreads), 1 << log_ctas,
-                         (size_t)part_len / 8 + 4 + (size_t)a.K * 12, s, args);
+                         (size_t)part_len / 8 + 4 + (size_t)a.K * 12, s, args, false);
 }
 
 template <typename T>

@@ -20,6 +20,7 @@
 // rewrites only the listed tokens from a hash table (123 us: scattered reads and partial
 // sectors from HBM), a list of the distinct tokens of a slice (115 us: atomics that
 // return), slices of 8192 tokens (114 us).
+#include <algorithm>
 #include <cmath>
 
 #include "sm103.cuh"
@@ -29,7 +30,7 @@ namespace {
 
 constexpr uint32_t kPromptBit = 0x80000000u, kBiasBit = 0x40000000u;  // of a token's count
 constexpr uint32_t kCountBits = kBiasBit - 1;
-constexpr int kMinLogSlice = 11, kMaxLogSlice = 14;  // tokens of a block, a power of two
+constexpr int kMinSlice = 2048, kMaxSlice = 18 * 1024;  // tokens of a block, a multiple of 1024
 constexpr int kLogitThreads = 256, kLogitBlocks = 3;
 constexpr int kBatch = 4;                            // steps whose loads are in flight together
 
@@ -44,7 +45,7 @@ struct LogitsArgs {
   const uint32_t* mask;
   int64_t mask_stride;
   uint32_t* status;
-  int log_slice;
+  int32_t slice;
 };
 
 // [start, end) of request b's list, empty (and reported) if the offsets are malformed.
@@ -85,36 +86,48 @@ __device__ __forceinline__ void count_token(uint32_t count, uint32_t off, uint32
                  : "memory");
 }
 
-// Counts the tokens [v0, v0 + len) among n ids at count[v - v0]; returns whether an id is
-// outside the vocabulary. An id is compared by its halves: the high one has to be 0.
-template <bool kOutput>
-__device__ __forceinline__ bool count_ids(const int64_t* ids, int32_t n, uint32_t V, uint32_t v0, uint32_t len,
-                                          uint32_t count) {
-  constexpr int kAhead = 8;  // ids in flight
-  const uint2* p = reinterpret_cast<const uint2*>(ids) + threadIdx.x;
+// Counts a request's tokens [v0, v0 + len) at count[v - v0], from `pn` prompt and `on`
+// output ids; returns whether an id is outside the vocabulary. An id is compared by its
+// halves: the high one has to be 0. The loads of both lists' last pieces (most lists are
+// no longer) go out together.
+__device__ __forceinline__ bool count_ids(const int64_t* p_ids, int32_t pn, const int64_t* o_ids, int32_t on, uint32_t V,
+                                          uint32_t v0, uint32_t len, uint32_t count) {
+  constexpr int kAhead = 8;  // ids of a list in flight
+  constexpr int32_t kRound = kLogitThreads * kAhead;
   uint32_t high = 0, most = 0;  // over all ids
-  auto one = [&](uint2 id) {
+  auto one = [&](uint2 id, bool output) {
     high |= id.y;
     most = max(most, id.x);
-    count_token<kOutput>(count, id.y ? 0xffffffffu : id.x - v0, len);
+    const uint32_t off = id.y ? 0xffffffffu : id.x - v0;
+    if (output)
+      count_token<true>(count, off, len);
+    else
+      count_token<false>(count, off, len);
   };
-  int32_t left = n;  // the same for the whole block
-  for (; left >= kLogitThreads * kAhead; left -= kLogitThreads * kAhead, p += kLogitThreads * kAhead) {
-    uint2 id[kAhead];
+  const uint2* p = reinterpret_cast<const uint2*>(p_ids) + threadIdx.x;
+  const uint2* o = reinterpret_cast<const uint2*>(o_ids) + threadIdx.x;
+  uint2 id[kAhead];
+  auto round = [&](const uint2* q, bool output) {
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) id[k] = __ldg(p + k * kLogitThreads);
+    for (int k = 0; k < kAhead; ++k) id[k] = __ldg(q + k * kLogitThreads);
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) one(id[k]);
-  }
-  if (left > 0) {
-    uint2 id[kAhead];
+    for (int k = 0; k < kAhead; ++k) one(id[k], output);
+  };
+  for (; pn >= kRound; pn -= kRound, p += kRound) round(p, false);
+  for (; on >= kRound; on -= kRound, o += kRound) round(o, true);
+  uint2 id2[kAhead];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if ((int)threadIdx.x + k * kLogitThreads < left) id[k] = __ldg(p + k * kLogitThreads);
+  for (int k = 0; k < kAhead; ++k)
+    if ((int)threadIdx.x + k * kLogitThreads < pn) id[k] = __ldg(p + k * kLogitThreads);
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if ((int)threadIdx.x + k * kLogitThreads < left) one(id[k]);
-  }
+  for (int k = 0; k < kAhead; ++k)
+    if ((int)threadIdx.x + k * kLogitThreads < on) id2[k] = __ldg(o + k * kLogitThreads);
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k)
+    if ((int)threadIdx.x + k * kLogitThreads < pn) one(id[k], false);
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k)
+    if ((int)threadIdx.x + k * kLogitThreads < on) one(id2[k], true);
   return high != 0 || most >= V;
 }
 
@@ -123,8 +136,7 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitBlocks) k_logits(LogitsAr
   extern __shared__ __align__(16) uint32_t smem[];
   __shared__ int repeated;  // a bias list names a token twice
   const int32_t b = blockIdx.y;
-  const int32_t slice = 1 << a.log_slice;
-  const int32_t v0 = (int32_t)blockIdx.x << a.log_slice, len = min(a.V - v0, slice);
+  const int32_t v0 = (int32_t)blockIdx.x * a.slice, len = min(a.V - v0, a.slice);
   const in_t* z = static_cast<const in_t*>(a.z) + b * a.z_stride + v0;
   out_t* y = static_cast<out_t*>(a.y) + b * a.y_stride + v0;
   // Groups of eight start `head` tokens into the slice, so that stores are 16-byte
@@ -162,19 +174,27 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitBlocks) k_logits(LogitsAr
   };
 #pragma unroll
   for (int u = 0; u < kBatch; ++u) load(u, threadIdx.x + u * kLogitThreads);
+  // a thread's first bias: its token, logit and value, ahead of their use
+  int64_t own_id = -1;
+  float own_z = 0.f, own_bias = 0.f;
+  if (kLists && bs + threadIdx.x < be) {
+    own_id = a.b_ids[bs + threadIdx.x];
+    own_bias = a.b_val[bs + threadIdx.x];
+  }
   if (kLists) {
     uint4* c4 = reinterpret_cast<uint4*>(smem);
-    for (int32_t i = threadIdx.x; i < slice / 4 + 1; i += kLogitThreads) c4[i] = make_uint4(0, 0, 0, 0);
+    for (int32_t i = threadIdx.x; i < a.slice / 4 + 1; i += kLogitThreads) c4[i] = make_uint4(0, 0, 0, 0);
     if (threadIdx.x == 0) repeated = 0;
     __syncthreads();
-    bool bad = count_ids<false>(a.p_ids + ps, (int32_t)(pe - ps), a.V, v0, len, smem_u32(count));
-    bad |= count_ids<true>(a.o_ids + os, (int32_t)(oe - os), a.V, v0, len, smem_u32(count));
+    bool bad = count_ids(a.p_ids + ps, (int32_t)(pe - ps), a.o_ids + os, (int32_t)(oe - os), a.V, v0, len,
+                         smem_u32(count));
     for (int64_t j = bs + threadIdx.x; j < be; j += kLogitThreads) {
-      const int64_t v = a.b_ids[j];
+      const int64_t v = j == bs + threadIdx.x ? own_id : a.b_ids[j];
       bad |= v < 0 || v >= a.V;
       if (v >= v0 && v < v0 + len && (atomicOr(&count[v - v0], kBiasBit) & kBiasBit)) repeated = 1;
     }
     if (bad) report(a.status, kErrIndex);
+    if (own_id >= v0 && own_id < v0 + len) own_z = Elem<in_t>::get(z[own_id - v0]);
     __syncthreads();
   }
   for (int32_t i0 = threadIdx.x; i0 < groups; i0 += kBatch * kLogitThreads) {
@@ -224,13 +244,14 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitBlocks) k_logits(LogitsAr
   }
   // Each biased token by the thread of its first entry; its biases in list order.
   for (int64_t j = bs + threadIdx.x; j < be; j += kLogitThreads) {
-    const int64_t v = a.b_ids[j];
+    const bool first = j == bs + threadIdx.x;
+    const int64_t v = first ? own_id : a.b_ids[j];
     if (v < v0 || v >= v0 + len) continue;
     bool mine = true;
     if (repeated)
       for (int64_t i = bs; i < j && mine; ++i) mine = a.b_ids[i] != v;
     if (!mine) continue;
-    float x = penalty(Elem<in_t>::get(z[v - v0]), count[v - v0]) + a.b_val[j];
+    float x = penalty(first ? own_z : Elem<in_t>::get(z[v - v0]), count[v - v0]) + (first ? own_bias : a.b_val[j]);
     if (repeated)
       for (int64_t i = j + 1; i < be; ++i)
         if (a.b_ids[i] == v) x += a.b_val[i];
@@ -241,20 +262,21 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitBlocks) k_logits(LogitsAr
 template <typename in_t, typename out_t>
 cudaError_t launch(int device, LogitsArgs& a, cudaStream_t s) {
   void* args[] = {&a};
-  // Slices of 16384 tokens (64 KB of counts, three CTAs an SM); fewer rows take smaller
-  // ones, down to 2048, until the GPU has two CTAs an SM.
-  int log_slice = kMaxLogSlice;
-  while (log_slice > kMinLogSlice && (((int64_t)a.V * a.B) >> log_slice) < 2 * sm_count(device)) --log_slice;
-  a.log_slice = log_slice;
-  const dim3 grid((a.V + (1 << log_slice) - 1) >> log_slice, a.B);
+  // Slices as large as three blocks an SM have room to count, of a size that fills whole
+  // waves of them: the fewest waves that such slices allow.
+  const int64_t slots = (int64_t)kLogitBlocks * sm_count(device);
+  const int64_t least = (a.V + kMaxSlice - 1) / kMaxSlice, waves = (least * a.B + slots - 1) / slots;
+  const int64_t a_row = waves * slots / a.B;  // slices of a row, at least `least`
+  a.slice = std::max(kMinSlice, (int32_t)(((a.V + a_row - 1) / a_row + 1023) / 1024 * 1024));
+  const dim3 grid((a.V + a.slice - 1) / a.slice, a.B);
   if (!a.p_ids && !a.o_ids && !a.b_ids)
     return launch_kernel(reinterpret_cast<const void*>(&k_logits<in_t, out_t, false>), grid, dim3(kLogitThreads), 0, s,
                          args, false);
   const void* fn = reinterpret_cast<const void*>(&k_logits<in_t, out_t, true>);
   static bool ready[64];
-  const cudaError_t e = allow_smem(fn, ((1 << kMaxLogSlice) + 4) * 4, device, ready);
+  const cudaError_t e = allow_smem(fn, (kMaxSlice + 4) * 4, device, ready);
   if (e != cudaSuccess) return e;
-  return launch_kernel(fn, grid, dim3(kLogitThreads), ((1 << log_slice) + 4) * 4, s, args, false);
+  return launch_kernel(fn, grid, dim3(kLogitThreads), (a.slice + 4) * 4, s, args, false);
 }
 
 template <typename in_t>

@@ -41,6 +41,7 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&x)[kGroup]) {
 template <typename T, int kFormat>
 __global__ void __launch_bounds__(kThreads) k_micro_quantize(QuantArgs a, int log_team) {
   constexpr int n = micro_block(kFormat), lanes = n / kGroup;  // lanes of a block
+  pdl_trigger();  // what reads the codes next waits for this kernel's end by itself
   const int32_t tiles = micro_tiles(a.K, kFormat), units = tiles * 4 * lanes;
   const int64_t row_bytes = micro_row_bytes(a.K);
   const int32_t team = 1 << log_team, lane = threadIdx.x & 31;

@@ -129,6 +129,7 @@ __global__ void __launch_bounds__(kMatmulThreads, 1)
     __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, ctl.tmem, 0);
+  pdl_wait();  // operands may come from the kernel before; it may still read the output's buffer
 
   if (warp == 4 && lane == 0) {
     uint32_t s = 0, round = 0;
@@ -277,8 +278,8 @@ cudaError_t launch(int device, MatmulArgs a, const Operands& o, cudaStream_t s) 
   const int64_t tiles = (a.N + rows - 1) / rows * ((a.M + kTok - 1) / kTok), most = sm_count(device) / S::kCtas;
   const unsigned grid = (unsigned)(tiles < most ? tiles : most) * S::kCtas;
   void* args[] = {&wmap, &wsmap, &xmap, &xsmap, &a};
-  return kPair ? launch_clusters(fn, dim3(grid), dim3(kMatmulThreads), 2, S::kSmem, s, args)
-               : launch_kernel(fn, dim3(grid), dim3(kMatmulThreads), S::kSmem, s, args, false);
+  return kPair ? launch_clusters(fn, dim3(grid), dim3(kMatmulThreads), 2, S::kSmem, s, args, true)
+               : launch_kernel(fn, dim3(grid), dim3(kMatmulThreads), S::kSmem, s, args, true);
 }
 
 template <typename T, int kFormat>

@@ -78,8 +78,14 @@ def _out_like(out, dev, rows, cols, dtype, name="out"):
     return code, stride
 
 
+_functions = {}  # of the library, by name
+
+
 def _call(name, *args):
-    st = getattr(E.load(), name)(*args)
+    f = _functions.get(name)
+    if f is None:
+        f = _functions[name] = getattr(E.load(), name)
+    st = f(*args)
     if st:
         raise E.EmbError(st, name)
 
@@ -107,7 +113,7 @@ def process_logits(logits, *, prompt=None, output=None, repetition=None, frequen
             raise ValueError(f"mask must be an int32 [{B}, {(V + 31) // 32}] tensor on cuda:{dev}")
         mp, ms = mask.data_ptr(), mask.stride(0)
     if out is None:
-        out = logits.new_empty((B, V), dtype=dtype)
+        out = torch.empty((B, V), dtype=dtype or logits.dtype, device=logits.device)
         yc, ys = _DTYPE.get(out.dtype, -1), V
     else:
         yc, ys = _out_like(out, dev, B, V, dtype)
@@ -135,7 +141,7 @@ def _gradient(logits, out, dev, N, V):
     if out is not None:
         return out, _out_like(out, dev, N, V, logits.dtype)[1]
     stride = max(logits.stride(0), V)
-    return logits.new_empty_strided((N, V), (stride, 1)), stride
+    return torch.empty_strided((N, V), (stride, 1), dtype=logits.dtype, device=logits.device), stride
 
 
 def distill_forward(logits, teacher_ids, teacher_logits, *, temperature=1.0, teacher_lse=None, status=None):
@@ -145,8 +151,8 @@ def distill_forward(logits, teacher_ids, teacher_logits, *, temperature=1.0, tea
     exp(logit / temperature), to count its mass off the list; without it the list is renormalised.
     """
     dev, N, V, rows = _rows_and_lists(logits, teacher_ids, teacher_logits)
-    loss = logits.new_empty(N, dtype=_F32)
-    stats = logits.new_empty((N, 4), dtype=_F32)
+    loss = torch.empty(N, dtype=_F32, device=logits.device)
+    stats = torch.empty((N, 4), dtype=_F32, device=logits.device)
     _call("emb_distill_forward", *rows, _vector(teacher_lse, dev, _F32, N, "teacher_lse"), temperature,
           loss.data_ptr(), stats.data_ptr(), _status(status, dev), _raw_stream(dev))
     return loss, stats
@@ -167,7 +173,7 @@ def distill_step(logits, teacher_ids, teacher_logits, row_weight=None, *, temper
                  status=None):
     """(loss [N], row_weight[n] * dloss[n] / dlogits) in one call; ``out`` may be ``logits``."""
     dev, N, V, rows = _rows_and_lists(logits, teacher_ids, teacher_logits)
-    loss = logits.new_empty(N, dtype=_F32)
+    loss = torch.empty(N, dtype=_F32, device=logits.device)
     out, stride = _gradient(logits, out, dev, N, V)
     _call("emb_distill_step", *rows, _vector(teacher_lse, dev, _F32, N, "teacher_lse"),
           _vector(row_weight, dev, _F32, N, "row_weight"), temperature, loss.data_ptr(), out.data_ptr(), stride,
@@ -245,8 +251,8 @@ def micro_quantize(x, format="mx", tensor_scale=1.0, *, out=None):
     if fmt is None:
         raise ValueError(f"format must be 'mx' or 'nv', got {format!r}")
     if out is None:
-        codes = x.new_empty((R, _row_bytes(K)), dtype=torch.uint8)
-        scales = x.new_empty(((R + 127) // 128, _tiles(K, format), 32, 4, 4), dtype=torch.uint8)
+        codes = torch.empty((R, _row_bytes(K)), dtype=torch.uint8, device=x.device)
+        scales = torch.empty(((R + 127) // 128, _tiles(K, format), 32, 4, 4), dtype=torch.uint8, device=x.device)
         out = MicroMatrix(codes, scales, R, K, format, tensor_scale)
     else:
         if (out.rows, out.cols, out.format, out._check("out")[0]) != (R, K, format, dev):
@@ -262,7 +268,7 @@ def micro_lookup(table, ids=None, *, dtype=torch.float32, out=None, status=None)
     dev, fmt, codes, scales = table._check("table")
     n = table.rows if ids is None else ids.numel()
     if out is None:
-        out = table.codes.new_empty((n, table.cols), dtype=dtype)
+        out = torch.empty((n, table.cols), dtype=dtype, device=table.codes.device)
         oc, stride = _DTYPE.get(dtype, -1), table.cols
     else:
         oc, stride = _out_like(out, dev, n, table.cols, None)
@@ -279,7 +285,7 @@ def micro_matmul(x, w, *, dtype=torch.bfloat16, out=None, status=None):
         raise ValueError("x and w must have the same format, columns and device")
     M, N = x.rows, w.rows
     if out is None:
-        out = x.codes.new_empty((M, N), dtype=dtype)
+        out = torch.empty((M, N), dtype=dtype, device=x.codes.device)
         oc, stride = _DTYPE.get(dtype, -1), N
     else:
         oc, stride = _out_like(out, dev, M, N, None)
