@@ -1,4 +1,5 @@
-"""Builds libembbwd.so in-tree: every csrc/*.cu compiled for sm_103a in parallel, then linked.
+"""Builds libembbwd.so in-tree: every csrc/*.cu compiled for sm_103a in parallel, then linked;
+and _vocab.so, the Python entry of the vocabulary operators (csrc/vocab_torch.cpp), beside it.
 
     python -m sparse_embedding_bag_gb300.build [--force] [--ptxas-v]
 """
@@ -16,6 +17,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libembbwd.so")
+ENTRY_SRC = os.path.join(CSRC, "vocab_torch.cpp")
+ENTRY = os.path.join(PKG, "_vocab.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE]
 
@@ -27,6 +30,28 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
+def build_entry() -> str:
+    """_vocab.so: host code against this machine's PyTorch headers (no link to libembbwd: it is
+    given the functions' addresses when it is loaded)."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    include = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"],
+               os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = ENTRY + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(x for p in include for x in ("-isystem", p)), ENTRY_SRC, "-o", tmp, "-L" + lib, "-Wl,-rpath," + lib,
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {ENTRY_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, ENTRY)
+    return ENTRY
+
+
 def _newest(paths):
     return max(os.path.getmtime(p) for p in paths)
 
@@ -34,7 +59,8 @@ def _newest(paths):
 def build(force: bool = False, ptxas_verbose: bool = False, jobs: int | None = None) -> str:
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     deps = srcs + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _newest(deps + [__file__]):
+    newest = _newest(deps + [ENTRY_SRC, __file__])
+    if not force and all(os.path.exists(p) and os.path.getmtime(p) >= newest for p in (LIB, ENTRY)):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -49,8 +75,10 @@ def build(force: bool = False, ptxas_verbose: bool = False, jobs: int | None = N
         return obj, r.stderr
 
     jobs = jobs or min(len(srcs), os.cpu_count() or 4)
-    with cf.ThreadPoolExecutor(jobs) as ex:
+    with cf.ThreadPoolExecutor(jobs + 1) as ex:
+        entry = ex.submit(build_entry)
         results = list(ex.map(compile_one, srcs))
+        entry.result()
     if ptxas_verbose:
         for _, log in results:
             sys.stderr.write(log)
