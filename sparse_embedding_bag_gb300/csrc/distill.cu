@@ -53,13 +53,19 @@ struct DistillArgs {
   int64_t t_stride;
   const float* lse;      // nullable: renormalise over the list
   const float* weight;   // nullable: 1
-  float tau, c2;         // c2 = log2(e) / tau
+  float tau, inv_tau, c2;  // c2 = log2(e) / tau
   float* loss;
   float4* stats;         // written by the forward, read by the backward
   void* dz;
   int64_t dz_stride;
   uint32_t* status;
 };
+
+// t_k / tau, as a product with the reciprocal, rounded: what is subtracted from it later
+// must not meet an unrounded product where L came from rounded ones.
+__device__ __forceinline__ float teacher_logit(const DistillArgs& a, int32_t n, int k) {
+  return __fmul_rn(load_as_float(a.t, a.t_dtype, n * a.t_stride + k), a.inv_tau);
+}
 
 // The teacher's list of a row in shared memory.
 struct List {
@@ -108,7 +114,7 @@ __device__ __forceinline__ bool read_list(const DistillArgs& a, int32_t n, List&
   float big = -INFINITY;
   for (int k = threadIdx.x; k < a.K; k += blockDim.x) {
     const int32_t id = l.id[k];
-    const float t = id >= 0 ? __fdiv_rn(load_as_float(a.t, a.t_dtype, n * a.t_stride + k), a.tau) : -INFINITY;
+    const float t = id >= 0 ? teacher_logit(a, n, k) : -INFINITY;
     l.z[k] = id >= lo && id < hi ? Elem<T>::get(z[id]) : 0.f;
     l.q[k] = t;
     big = fmaxf(big, t);
@@ -140,8 +146,8 @@ __device__ __forceinline__ float loss_of(const DistillArgs& a, int32_t n, const 
   float ls = 0.f;
   for (int k = threadIdx.x; k < a.K; k += blockDim.x)
     if (l.q[k] > 0.f) {
-      const float logp = (l.z[k] - M) * (a.c2 * kLn2) - logS;
-      ls += l.q[k] * ((__fdiv_rn(load_as_float(a.t, a.t_dtype, n * a.t_stride + k), a.tau) - L) - logp);
+      const float logp = __fmul_rn(l.z[k] - M, a.inv_tau) - logS;
+      ls += l.q[k] * ((teacher_logit(a, n, k) - L) - logp);
     } else if (!(l.q[k] == 0.f)) {
       ls = NAN;
     }
@@ -474,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks) k_distill_backward(Disti
       continue;
     }
     l.id[k] = e;
-    l.q[k] = expf(__fdiv_rn(load_as_float(a.t, a.t_dtype, n * a.t_stride + k), a.tau) - st.w);
+    l.q[k] = expf(teacher_logit(a, n, k) - st.w);
     l.z[k] = Elem<T>::get(z[e]);
     if (atomicOr(&bitmap[e >> 5], 1u << (e & 31)) >> (e & 31) & 1u) l.repeated = 1;
   }
@@ -546,6 +552,7 @@ emb_status distill(int device, int mode, int dtype, DistillArgs a, void* stream)
     if (!a.dz || !aligned(a.dz, dtype_size(dtype)) || (a.N > 1 && a.dz_stride < a.V)) return EMB_ERR_INVALID_ARG;
     if (a.dz == a.z && a.N > 1 && a.dz_stride != a.z_stride) return EMB_ERR_INVALID_ARG;
   }
+  a.inv_tau = 1.f / a.tau;
   a.c2 = (float)(1.4426950408889634 / (double)a.tau);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return on_device(device, [&] {

@@ -74,9 +74,6 @@ __device__ __forceinline__ void store8(T* p, const float (&x)[kGroup]) {
 
 constexpr int32_t kMaxVocab = 1 << 20;  // widest row of logits
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-
 // Sums (maxima) over a block of up to 1024 threads, the same for every thread.
 // `scratch` holds 33 floats. The order of additions is fixed. fmaxf drops NaN:
 // a NaN among the values has to reach the result by another way (a sum).
