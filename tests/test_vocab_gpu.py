@@ -476,3 +476,95 @@ def test_repeated_calls_give_the_same_bits(V):
     for _ in range(5):
         again = (V.process_logits(z, output=hist, frequency=freq, bias=bias), *V.distill_step(z, dev(ids), dev(t)))
         assert all(torch.equal(a, b) for a, b in zip(again, first))
+
+
+def test_the_bindings_of_the_c_abi_give_the_same(V):
+    from sparse_embedding_bag_gb300 import embbwd as E
+    z = torch.randn(3, 400, device="cuda")
+    ids, t = torch.randint(0, 400, (3, 5), device="cuda"), torch.randn(3, 5, device="cuda")
+    hist, off = csr([[1, 2, 2], [], [399]])
+    rep, w = torch.full((3,), 1.5, device="cuda"), torch.rand(3, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, loss, stats = torch.empty_like(z), torch.empty(3, device="cuda"), torch.empty(3, 4, device="cuda")
+    E.emb_logits_process(0, z, 0, 400, 3, 400, None, None, 0, hist, off, 4, rep, None, None, None, None, None, 0, None, 0,
+                         out, 0, 400, status)
+    assert torch.equal(out, V.process_logits(z, output=(hist, off), repetition=rep))
+    E.emb_distill_forward(0, z, 0, 400, 3, 400, ids, t, 0, 5, 5, None, 2.0, loss, stats, status)
+    want = V.distill_forward(z, ids, t, temperature=2.0)
+    assert torch.equal(loss, want[0]) and torch.equal(stats, want[1])
+    E.emb_distill_backward(0, z, 0, 400, 3, 400, ids, t, 0, 5, 5, stats, w, 2.0, out, 400, status)
+    assert torch.equal(out, V.distill_backward(z, ids, t, stats, w, temperature=2.0))
+    E.emb_distill_step(0, z, 0, 400, 3, 400, ids, t, 0, 5, 5, None, w, 2.0, loss, out, 400, status)
+    want = V.distill_step(z, ids, t, w, temperature=2.0)
+    assert torch.equal(loss, want[0]) and torch.equal(out, want[1])
+    m = V.micro_quantize(z, "nv", 0.01)
+    codes, scales = torch.empty_like(m.codes), torch.empty_like(m.scales)
+    E.emb_micro_quantize(0, z, 0, 400, 3, 400, E.EMB_MICRO_NV, 0.01, codes, scales)
+    assert torch.equal(codes, m.codes) and torch.equal(scales, m.scales)
+    E.emb_micro_lookup(0, codes, scales, 3, 400, E.EMB_MICRO_NV, 0.01, None, 3, out, 0, 400, status)
+    assert torch.equal(out, V.micro_lookup(m))
+    y = torch.empty(3, 3, device="cuda")
+    E.emb_micro_matmul(0, codes, scales, 0.01, 3, codes, scales, 0.01, 3, 400, E.EMB_MICRO_NV, y, 0, 3, status)
+    assert torch.equal(y, V.micro_matmul(m, m, dtype=torch.float32)) and status.item() == 0
+    with pytest.raises(E.EmbError):
+        E.emb_micro_matmul(0, codes, scales, -1.0, 3, codes, scales, 0.01, 3, 400, E.EMB_MICRO_NV, y, 0, 3, status)
+    with pytest.raises(E.EmbError):
+        V.distill_step(z, ids, t, temperature=0.0)
+
+
+def test_bindings_refuse_what_does_not_fit(V):
+    z, ids, t = torch.randn(3, 400, device="cuda"), torch.zeros(3, 5, dtype=torch.int64, device="cuda"), \
+        torch.randn(3, 5, device="cuda")
+    m = V.micro_quantize(z)
+    bad = [
+        lambda: V.process_logits(z.double()), lambda: V.process_logits(z[0]), lambda: V.process_logits(z.t()),
+        lambda: V.process_logits(z, repetition=torch.ones(2, device="cuda")),
+        lambda: V.process_logits(z, repetition=torch.ones(3)),
+        lambda: V.process_logits(z, prompt=(ids[0], ids[0])),
+        lambda: V.process_logits(z, prompt=(ids[0].int(), ids[0, :4])),
+        lambda: V.process_logits(z, bias=(ids[0], ids[0, :4])),
+        lambda: V.process_logits(z, mask=torch.zeros(3, 12, dtype=torch.int32, device="cuda")),
+        lambda: V.process_logits(z, mask=torch.zeros(3, 13, device="cuda")),
+        lambda: V.process_logits(z, out=z[:, :399]), lambda: V.process_logits(z, dtype=torch.float64),
+        lambda: V.process_logits(z, out=z, dtype=torch.bfloat16), lambda: V.process_logits(z, status=t),
+        lambda: V.distill_step(z, ids.int(), t), lambda: V.distill_step(z, ids[:2], t[:2]),
+        lambda: V.distill_step(z, ids, t[:, :4]), lambda: V.distill_step(z, ids, t.double()),
+        lambda: V.distill_step(z, ids, t, out=z.bfloat16()), lambda: V.distill_step(z, ids, t, torch.ones(4, device="cuda")),
+        lambda: V.distill_step(z, ids, t, teacher_lse=torch.ones(3)), lambda: V.distill_backward(z, ids, t, t),
+        lambda: V.micro_quantize(z, "fp4"), lambda: V.micro_quantize(z.long()),
+        lambda: V.micro_quantize(z, "nv", 0.1, out=m), lambda: V.micro_quantize(z[:2], out=m),
+        lambda: V.micro_lookup(m, ids[0].int()), lambda: V.micro_lookup(m, out=z[:2]),
+        lambda: V.micro_lookup(m, dtype=torch.int32), lambda: V.micro_matmul(m, V.micro_quantize(z, "nv", 0.1)),
+        lambda: V.micro_matmul(m, V.micro_quantize(z[:, :64])), lambda: V.micro_matmul(m, m, out=z),
+        lambda: V.micro_matmul(m, V.MicroMatrix(m.codes, m.scales, 4, 400, "mx")),
+    ]
+    for i, f in enumerate(bad):
+        with pytest.raises(ValueError):
+            f()
+            pytest.fail(f"call {i} was accepted")
+
+
+def test_lm_head_serves_and_learns(V):
+    from sparse_embedding_bag_gb300 import lm_head
+    g = torch.Generator(device="cuda").manual_seed(3)
+    n_vocab, dim, N, K = 1003, 64, 48, 8
+    table = torch.randn((n_vocab, dim), generator=g, device="cuda") * 0.1
+    layer = torch.randn((dim, dim), generator=g, device="cuda") * dim ** -0.5
+    allowed = np.zeros((2, (n_vocab + 31) // 32 * 32), bool)
+    allowed[0, 500:520], allowed[1, [7, 1002]] = True, True
+    mask = torch.from_numpy(np.packbits(allowed, axis=1, bitorder="little").view(np.int32)).cuda()
+    for fmt in ("mx", "nv"):
+        out = lm_head.serve(table.bfloat16(), layer.bfloat16(), [[1, 2, 3], [4]], 5, format=fmt, mask=mask)
+        assert all(500 <= v < 520 for v in out[0]) and all(v in (7, 1002) for v in out[1])
+    tokens = torch.randint(0, n_vocab, (N,), generator=g, device="cuda")
+    ids = torch.stack([torch.randperm(n_vocab, generator=g, device="cuda")[:K] for _ in range(N)])
+    teacher = torch.randn((N, K), generator=g, device="cuda") * 2
+    ref_table = table.clone().requires_grad_()
+    losses = lm_head.distill(table, layer, tokens, ids, teacher, lr=5.0, steps=12)
+    assert losses[-1] < 0.8 * losses[0] and all(b < a for a, b in zip(losses, losses[1:]))
+    # the first loss, and through autograd the direction of the table's whole gradient
+    hidden = torch.tanh(ref_table[tokens] @ layer)
+    loss = V.distill_loss(hidden @ ref_table.t(), ids, teacher, temperature=2.0).mean()
+    assert abs(loss.item() - losses[0]) <= 1e-4 * losses[0]
+    loss.backward()
+    assert ((table - ref_table.detach()) * ref_table.grad).sum() < 0
