@@ -3,11 +3,14 @@
 // Both are bound by HBM traffic. A thread takes units of 8 elements, so that a warp's codes
 // are whole 128-byte lines and its 16-bit values whole 512-byte ones; a team of lanes (a
 // warp, or less for short rows) takes a piece of a row, kBatch loads of each lane in flight.
-// Measured at 128256 x 4096 (HBM bytes over time): bf16 to MX 244 us, 5.4 TB/s, to NV 305 us;
-// fp32 to MX 328 us, 7.3 TB/s; MX to bf16 253 us, 5.2 TB/s, to fp32 391 us, 6.1 TB/s.
+// Measured at 128256 x 4096 (HBM bytes over time): bf16 to MX 221 us, 6.0 TB/s, to NV 265 us;
+// fp32 to MX 334 us, 7.1 TB/s; MX or NV to bf16 208 us, 6.4 TB/s, to fp32 438 us, 5.4 TB/s.
+// 16-bit types are nearly bound by instructions (the conversions run at a quarter of the
+// rate): checking every unit's place in its row took 10 % more.
 #include <cmath>
 
 #include "micro.cuh"
+#include "sm103.cuh"
 
 namespace embbwd {
 namespace {
@@ -39,8 +42,8 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&x)[kGroup]) {
 }
 
 // Rows and blocks are taken up to whole scale tiles, whose padding is zero. Rows that do not
-// start at 16 bytes are read element by element from L1 (128256 x 4096 bf16 to MX: 408 us
-// against 244); reading the aligned pieces that cover them and shifting took 555 us.
+// start at 16 bytes are read element by element from L1 (128256 x 4096 bf16 to MX: 454 us
+// against 221); reading the aligned pieces that cover them and shifting took 555 us.
 template <typename T, int kFormat>
 __global__ void __launch_bounds__(kThreads) k_micro_quantize(QuantArgs a, int log_team) {
   constexpr int n = micro_block(kFormat), lanes = n / kGroup;  // lanes of a block
@@ -51,23 +54,26 @@ __global__ void __launch_bounds__(kThreads) k_micro_quantize(QuantArgs a, int lo
   const int64_t r = (int64_t)blockIdx.x * (kThreads >> log_team) + (threadIdx.x >> log_team);
   const int32_t u0 = (int32_t)blockIdx.y * kBatch * team + (threadIdx.x & (team - 1));
   const T* x = static_cast<const T*>(a.x) + r * a.x_stride;
-  const bool wide = reinterpret_cast<uintptr_t>(x) % 16 == 0;
+  const bool row = r < a.R, wide = row && reinterpret_cast<uintptr_t>(x) % 16 == 0;
+  // Are all of this team's units whole and loaded 16 bytes at a time? Then nothing is checked.
+  const bool plain = wide && ((int32_t)blockIdx.y + 1) * kBatch * team * kGroup <= a.K;
   Raw8<T> raw[kBatch];
 #pragma unroll
   for (int b = 0; b < kBatch; ++b) {
     const int32_t k = (u0 + b * team) * kGroup;
-    if (r < a.R && wide && k + kGroup <= a.K) raw[b].load(x + k);
+    if (plain || (wide && k + kGroup <= a.K)) raw[b].load(x + k);
   }
-#pragma unroll
-  for (int b = 0; b < kBatch; ++b) {
+  uint8_t* codes = a.codes + r * row_bytes + u0 * 4;
+  uint8_t* word_at = a.scales + micro_scale_at(r, u0 / lanes, tiles);
+  const bool writes_word = lane % (4 * lanes) == 0 && r < (a.R + 127) / 128 * 128;
+  auto unit = [&](int b, bool checked) {
     const int32_t u = u0 + b * team, k = u * kGroup;
-    if (b > 0 && (int32_t)blockIdx.y * kBatch * team + b * team >= units) break;  // the same for the whole block
     float v[kGroup];
-    if (r < a.R && wide && k + kGroup <= a.K) {
+    if (!checked || (wide && k + kGroup <= a.K)) {
       raw[b].widen(v);
     } else {
 #pragma unroll
-      for (int i = 0; i < kGroup; ++i) v[i] = r < a.R && k + i < a.K ? Elem<T>::get(x[k + i]) : 0.f;
+      for (int i = 0; i < kGroup; ++i) v[i] = row && k + i < a.K ? Elem<T>::get(x[k + i]) : 0.f;
     }
     // the largest magnitude by its bits: infinity is above all numbers, NaN above infinity
     uint32_t most = 0;
@@ -77,16 +83,29 @@ __global__ void __launch_bounds__(kThreads) k_micro_quantize(QuantArgs a, int lo
     for (int o = 1; o < lanes; o *= 2) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
     float f;
     const uint32_t byte = micro_scale<kFormat>(__uint_as_float(most), a.g, &f);
+    const F2 f2 = F2::of(f, f);
 #pragma unroll
-    for (int i = 0; i < kGroup; ++i) v[i] *= f;
-    const uint32_t codes = most >= 0x7f800000u ? 0u : e2m1x8(v);
-    if (r < a.R && (int64_t)u * 4 < row_bytes) *reinterpret_cast<uint32_t*>(a.codes + r * row_bytes + u * 4) = codes;
+    for (int i = 0; i < kGroup; i += 2) {
+      const float2 y = (F2::of(v[i], v[i + 1]) * f2).get();
+      v[i] = y.x, v[i + 1] = y.y;
+    }
+    const uint32_t eight = most >= 0x7f800000u ? 0u : e2m1x8(v);
+    if (!checked || (row && (int64_t)u * 4 < row_bytes)) *reinterpret_cast<uint32_t*>(codes + b * team * 4) = eight;
     // four blocks' bytes make one word of the scale tile
     uint32_t word = byte << ((lane / lanes & 3) * 8);
     word |= __shfl_xor_sync(0xffffffffu, word, lanes);
     word |= __shfl_xor_sync(0xffffffffu, word, 2 * lanes);
-    if (lane % (4 * lanes) == 0 && u < units && r < (a.R + 127) / 128 * 128)
-      *reinterpret_cast<uint32_t*>(a.scales + micro_scale_at(r, u / lanes, tiles)) = word;
+    if (writes_word && (!checked || u < units))
+      *reinterpret_cast<uint32_t*>(word_at + b * team / (4 * lanes) * 512) = word;
+  };
+  if (__all_sync(0xffffffffu, plain)) {
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) unit(b, false);
+  } else {
+    for (int b = 0; b < kBatch; ++b) {
+      if (b > 0 && ((int32_t)blockIdx.y * kBatch + b) * team >= units) break;  // the same for the whole block
+      unit(b, true);
+    }
   }
 }
 
@@ -108,8 +127,9 @@ __device__ __forceinline__ float micro_value(float v, float s, float g) {
   return kFormat == kMicroMX ? v * s : __fmul_rn(v * s, g);
 }
 
-// Units a thread has in flight: what it loads is small, what it stores decides. 128256 x 4096
-// MX to bf16: 253 us with 8, 272 with 4, 321 with 2; to fp32: 431, 454, 391.
+// Units a thread has in flight: what it loads is small, so that 16-bit outputs want many
+// (128256 x 4096 MX to bf16, before the units were cheaper: 253 us with 8, 272 with 4, 321
+// with 2); fp32 stores fill the queues by themselves (431, 454, 391).
 template <typename T>
 struct LookupBatch {
   static constexpr int value = sizeof(T) == 2 ? 8 : 2;
@@ -148,15 +168,27 @@ __global__ void __launch_bounds__(kThreads) k_micro_lookup(LookupArgs a, int log
   for (int b = 0; b < kBatch; ++b) {
     const int32_t u = u0 + b * team, k = head + u * kGroup;
     if (u >= units) break;
-    const uint32_t w = __funnelshift_r(word[b], next[b], head * 4);
-    const float s = micro_scale_value<kFormat>(byte[b]), s2 = head ? micro_scale_value<kFormat>(byte2[b]) : s;
-    const int32_t same = n - k % n;  // elements of the unit in its first block
+    const float s = micro_scale_value<kFormat>(byte[b]);
     float x[kGroup];
+    if (head == 0) {
+      const F2 s2 = F2::of(s, s), g2 = F2::of(a.g, a.g);
 #pragma unroll
-    for (int i = 0; i < kGroup; i += 2) {
-      const float2 v = e2m1x2_values(w >> 4 * i & 0xffu);
-      x[i] = micro_value<kFormat>(v.x, i < same ? s : s2, a.g);
-      x[i + 1] = micro_value<kFormat>(v.y, i + 1 < same ? s : s2, a.g);
+      for (int i = 0; i < kGroup; i += 2) {
+        const float2 v = e2m1x2_values(word[b] >> 4 * i & 0xffu);
+        F2 y = F2::of(v.x, v.y) * s2;
+        if (kFormat == kMicroNV) y = y * g2;
+        x[i] = y.get().x, x[i + 1] = y.get().y;
+      }
+    } else {
+      const uint32_t w = __funnelshift_r(word[b], next[b], head * 4);
+      const float s2 = micro_scale_value<kFormat>(byte2[b]);
+      const int32_t same = n - k % n;  // elements of the unit in its first block
+#pragma unroll
+      for (int i = 0; i < kGroup; i += 2) {
+        const float2 v = e2m1x2_values(w >> 4 * i & 0xffu);
+        x[i] = micro_value<kFormat>(v.x, i < same ? s : s2, a.g);
+        x[i + 1] = micro_value<kFormat>(v.y, i + 1 < same ? s : s2, a.g);
+      }
     }
     store8(out + k, x);
   }

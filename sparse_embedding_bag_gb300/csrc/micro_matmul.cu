@@ -19,7 +19,8 @@
 // With more than a few tokens, two CTAs work as a pair (kPair): 256 rows of the table
 // against kTok tokens, each CTA bringing its own rows and half of the tokens. What bounds
 // a large product is the way from L2 to the SMs, not the MMA: at 2048 x 128256 x 4096 (NV)
-// single CTAs of 128 x 256 moved 54 KB a stage and took 550 us, pairs 38 KB PAIR_US.
+// single CTAs of 128 x 256 moved 54 KB a stage and took 382 us, pairs 38 KB 375 us; both wait for L2 more than for the MMA (330 us
+// with the stores left out). Fetching the table's next rows to L2 a tile ahead cost 25 us.
 #include <cmath>
 
 #include "micro.cuh"
