@@ -129,10 +129,10 @@ __device__ __forceinline__ float micro_value(float v, float s, float g) {
 
 // Units a thread has in flight: what it loads is small, so that 16-bit outputs want many
 // (128256 x 4096 MX to bf16, before the units were cheaper: 253 us with 8, 272 with 4, 321
-// with 2); fp32 stores fill the queues by themselves (431, 454, 391).
+// with 2); fp32 stores fill the queues by themselves (now 425 us with 1, 438 with 2, 460 with 4).
 template <typename T>
 struct LookupBatch {
-  static constexpr int value = sizeof(T) == 2 ? 8 : 2;
+  static constexpr int value = sizeof(T) == 2 ? 8 : 1;
 };
 
 // Units start at the row's first 16-byte boundary of the output: stores are whole, and the
