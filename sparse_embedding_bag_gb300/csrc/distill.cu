@@ -338,6 +338,7 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks) k_distill_rows(DistillAr
   __shared__ List l;
   __shared__ float scratch[64];
   __shared__ float parts[3][kMaxCluster];  // of every CTA: largest logit, sums off and on the list
+  cluster_arrive();  // shared memory of a CTA is written by others only once it runs
   const uint32_t ctas = 1u << log_ctas, rank = blockIdx.x & (ctas - 1);
   const int32_t n = blockIdx.x >> log_ctas;
   const int32_t r0 = min((int64_t)a.V, (int64_t)rank * part_len), len = min(a.V - r0, part_len);
@@ -366,6 +367,8 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks) k_distill_rows(DistillAr
       if (!kGrad) a.stats[n] = make_float4(0.f, 1.f, 0.f, L);
     }
     if (kGrad) store_zeros(dz, len, Cut<T>(dz, len));
+    __syncwarp();
+    cluster_wait();
     return;
   }
   mark_list(a, l, bitmap, r0, len, first);
@@ -419,11 +422,14 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks) k_distill_rows(DistillAr
     if (l.id[k] >= 0 && e >= 0 && e < len && is_first(l, k)) top += ex2((l.z[k] - base) * a.c2);
   }
   block_sums(rest, top, scratch);
+  __syncwarp();
+  cluster_wait();
   if (threadIdx.x < ctas) {
     cluster_store(cluster_map(smem_u32(&parts[0][rank]), threadIdx.x), M);
     cluster_store(cluster_map(smem_u32(&parts[1][rank]), threadIdx.x), rest);
     cluster_store(cluster_map(smem_u32(&parts[2][rank]), threadIdx.x), top);
   }
+  __syncwarp();
   cluster_sync();
   float S = 0.f, off = 0.f;
   for (uint32_t i = 0; i < ctas; ++i) M = fmaxf(M, parts[0][i]);

@@ -238,6 +238,47 @@ def test_distill_whole_vocabulary_on_the_list_and_masked_logits(V):
     assert torch.isnan(loss[0]) and torch.isnan(g[0]).all()
 
 
+def test_distill_rows_at_the_lowest_value_of_their_type(V):
+    # masked throughout with finfo.min: as uniform as a row of equal logits
+    for dtype in DTYPES:
+        low = torch.finfo(getattr(torch, dtype)).min
+        ids, t = np.array([[1, 7, 300]]), np.array([[1.0, 0.5, 0.0]], np.float32)
+        lse = np.array([1.9], np.float32)
+        for tail in (None, dev(lse)):
+            got = V.distill_step(torch.full((1, 900), low, device="cuda", dtype=getattr(torch, dtype)), dev(ids), dev(t),
+                                 teacher_lse=tail)
+            want = V.distill_step(torch.zeros(1, 900, device="cuda", dtype=getattr(torch, dtype)), dev(ids), dev(t),
+                                  teacher_lse=tail)
+            assert torch.isfinite(got[0]).all() and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_rows_beyond_32_bit_offsets(V):
+    # three rows 2^31 elements apart
+    n_vocab, stride = 5003, 1 << 31
+    rng = np.random.default_rng(12)
+    flat = torch.empty(2 * stride + n_vocab, dtype=torch.bfloat16, device="cuda")
+    z = flat.as_strided((3, n_vocab), (stride, 1))
+    z.copy_(dev(rng.normal(0, 2, (3, n_vocab)), "bfloat16"))
+    near = z.clone(memory_format=torch.contiguous_format)
+    hist, rep = csr([[1, 2], [5, 5, 5], [5002]]), torch.full((3,), 1.5, device="cuda")
+    want = V.process_logits(near, output=hist, repetition=rep)
+    assert torch.equal(V.process_logits(z, output=hist, repetition=rep), want)
+    ids, t = teacher_lists(rng, 3, n_vocab, 9)
+    loss, g = V.distill_step(near, dev(ids), dev(t))
+    loss2, g2 = V.distill_step(z, dev(ids), dev(t), out=z)
+    close(f64(loss2), f64(loss), 1e-5 * np.abs(f64(loss)))
+    close(f64(g2), f64(g), 2.0 ** -7 * np.abs(f64(g)) + 1e-7)
+    z.copy_(near)
+    m = V.micro_quantize(z)
+    assert torch.equal(m.codes, V.micro_quantize(near).codes)
+    V.micro_lookup(m, out=z)
+    assert torch.equal(z, V.micro_lookup(m, dtype=torch.bfloat16))
+    y = V.micro_matmul(m, m)
+    wide = flat.as_strided((3, 3), (stride, 1))
+    V.micro_matmul(m, m, out=wide)
+    assert torch.equal(wide, y)
+
+
 def test_distill_student_sure_of_the_list(V):
     # the student's mass off the list is about 1e-12: u must not come from 1 - (mass on the list)
     rng = np.random.default_rng(5)
