@@ -344,6 +344,8 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks) k_distill_rows(DistillAr
   const int32_t r0 = min((int64_t)a.V, (int64_t)rank * part_len), len = min(a.V - r0, part_len);
   const T* z = static_cast<const T*>(a.z) + n * a.z_stride + r0;
   T* dz = kGrad ? static_cast<T*>(a.dz) + n * a.dz_stride + r0 : nullptr;
+  pdl_wait();
+  pdl_trigger();
   const Cut<T> cut(z, len);  // the order of the sums goes by the logits' alignment alone
   uint4 raw[kBatch];
   load_first<true>(z, cut, raw);
@@ -470,6 +472,8 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks) k_distill_backward(Disti
   const int32_t len = min(a.V - r0, piece);
   const T* z = static_cast<const T*>(a.z) + n * a.z_stride + r0;
   T* dz = static_cast<T*>(a.dz) + n * a.dz_stride + r0;
+  pdl_wait();
+  pdl_trigger();
   const Cut<T> cut(dz, len);
   uint4 raw[kBatch];
   load_first<kWide>(z, cut, raw);
@@ -526,7 +530,7 @@ cudaError_t launch_rows(int device, bool grad, DistillArgs& a, cudaStream_t s) {
                                       : reinterpret_cast<const void*>(&k_distill_rows<T, true, false>);
   void* args[] = {&a, &part_len, &log_ctas};
   return launch_clusters(fn, dim3((unsigned)a.N << log_ctas), dim3(kThreads), 1 << log_ctas,
-                         (size_t)part_len / 8 + 4 + (size_t)a.K * 12, s, args, false);
+                         (size_t)part_len / 8 + 4 + (size_t)a.K * 12, s, args, true);
 }
 
 template <typename T>
@@ -539,7 +543,7 @@ cudaError_t launch_mode(int device, int mode, DistillArgs& a, cudaStream_t s) {
   void* args[] = {&a, &pieces, &piece};
   const void* fn = wide_loads<T>(a) ? reinterpret_cast<const void*>(&k_distill_backward<T, true>)
                                     : reinterpret_cast<const void*>(&k_distill_backward<T, false>);
-  return launch_kernel(fn, dim3((unsigned)a.N * pieces), dim3(kThreads), (size_t)a.K * 12, s, args, false);
+  return launch_kernel(fn, dim3((unsigned)a.N * pieces), dim3(kThreads), (size_t)a.K * 12, s, args, true);
 }
 
 emb_status distill(int device, int mode, int dtype, DistillArgs a, void* stream) {

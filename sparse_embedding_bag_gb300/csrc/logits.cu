@@ -135,6 +135,8 @@ template <typename in_t, typename out_t, bool kLists>
 __global__ void __launch_bounds__(kLogitThreads, kLogitBlocks) k_logits(LogitsArgs a) {
   extern __shared__ __align__(16) uint32_t smem[];
   __shared__ int repeated;  // a bias list names a token twice
+  pdl_wait();
+  pdl_trigger();
   const int32_t b = blockIdx.y;
   const int32_t v0 = (int32_t)blockIdx.x * a.slice, len = min(a.V - v0, a.slice);
   const in_t* z = static_cast<const in_t*>(a.z) + b * a.z_stride + v0;
@@ -271,12 +273,12 @@ cudaError_t launch(int device, LogitsArgs& a, cudaStream_t s) {
   const dim3 grid((a.V + a.slice - 1) / a.slice, a.B);
   if (!a.p_ids && !a.o_ids && !a.b_ids)
     return launch_kernel(reinterpret_cast<const void*>(&k_logits<in_t, out_t, false>), grid, dim3(kLogitThreads), 0, s,
-                         args, false);
+                         args, true);
   const void* fn = reinterpret_cast<const void*>(&k_logits<in_t, out_t, true>);
   static bool ready[64];
   const cudaError_t e = allow_smem(fn, (kMaxSlice + 4) * 4, device, ready);
   if (e != cudaSuccess) return e;
-  return launch_kernel(fn, grid, dim3(kLogitThreads), (a.slice + 4) * 4, s, args, false);
+  return launch_kernel(fn, grid, dim3(kLogitThreads), (a.slice + 4) * 4, s, args, true);
 }
 
 template <typename in_t>

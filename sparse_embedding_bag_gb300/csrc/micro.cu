@@ -47,7 +47,8 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&x)[kGroup]) {
 template <typename T, int kFormat>
 __global__ void __launch_bounds__(kThreads) k_micro_quantize(QuantArgs a, int log_team) {
   constexpr int n = micro_block(kFormat), lanes = n / kGroup;  // lanes of a block
-  pdl_trigger();  // what reads the codes next waits for this kernel's end by itself
+  pdl_wait();
+  pdl_trigger();
   const int32_t tiles = micro_tiles(a.K, kFormat), units = tiles * 4 * lanes;
   const int64_t row_bytes = micro_row_bytes(a.K);
   const int32_t team = 1 << log_team, lane = threadIdx.x & 31;
@@ -140,6 +141,8 @@ struct LookupBatch {
 template <typename T, int kFormat>
 __global__ void __launch_bounds__(kThreads) k_micro_lookup(LookupArgs a, int log_team) {
   constexpr int n = micro_block(kFormat), out_n = 16 / sizeof(T), kBatch = LookupBatch<T>::value;
+  pdl_wait();
+  pdl_trigger();
   const int32_t team = 1 << log_team;
   const int64_t row = (int64_t)blockIdx.x * (kThreads >> log_team) + (threadIdx.x >> log_team);
   if (row >= a.n) return;
@@ -231,7 +234,7 @@ cudaError_t launch_teams(const void* fn, int64_t rows, int32_t units, int log_le
   const int64_t per_block = kThreads >> *log_team;
   const int32_t piece = batch << *log_team;
   return launch_kernel(fn, dim3((unsigned)((rows + per_block - 1) / per_block), (units + piece - 1) / piece),
-                       dim3(kThreads), 0, s, args, false);
+                       dim3(kThreads), 0, s, args, true);
 }
 
 }  // namespace

@@ -130,6 +130,7 @@ __global__ void __launch_bounds__(kMatmulThreads, 1)
     __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, ctl.tmem, 0);
+  pdl_trigger();
   pdl_wait();  // operands may come from the kernel before; it may still read the output's buffer
 
   if (warp == 4 && lane == 0) {
