@@ -28,9 +28,7 @@
 namespace embbwd {
 namespace {
 
-constexpr uint32_t kPromptBit = 0x80000000u, kBiasBit = 0x40000000u;  // of a token's count
-constexpr uint32_t kCountBits = kBiasBit - 1;
-constexpr int kMinSlice = 2048, kMaxSlice = 18 * 1024;  // tokens of a block, a multiple of 1024
+constexpr int kMinSlice = 2048, kMaxSlice = 36 * 1024;  // tokens of a block, a multiple of 1024
 constexpr int kLogitThreads = 256, kLogitBlocks = 3;
 constexpr int kBatch = 4;                            // steps whose loads are in flight together
 
@@ -48,6 +46,7 @@ struct LogitsArgs {
   int32_t slice;
 };
 
+
 // [start, end) of request b's list, empty (and reported) if the offsets are malformed.
 __device__ __forceinline__ void list_of(const int64_t* off, int64_t n, int32_t b, uint32_t* status, int64_t* start,
                                         int64_t* end) {
@@ -59,39 +58,72 @@ __device__ __forceinline__ void list_of(const int64_t* off, int64_t n, int32_t b
   }
 }
 
-// The request's penalties. A division by `repetition` is a multiplication by its
-// reciprocal (one more rounding in fp32), and nothing branches: a warp's 256 tokens are
-// rarely all unseen, and a branch for each with a division behind it cost 20 us at
-// 512 x 131071.
+// The request's penalties for a token seen `n` times in the output (0: only in the prompt).
+// A division by `repetition` is a multiplication by its reciprocal (one more rounding in
+// fp32), and nothing branches: a warp's 256 tokens are rarely all unseen, and a branch for
+// each with a division behind it cost 20 us at 512 x 131071.
 struct Penalty {
   float rep, inv, freq, pres;
-  __device__ __forceinline__ float operator()(float z, uint32_t c) const {
-    const uint32_t n = c & kCountBits;
-    const float y = c & ~kBiasBit ? z * (z > 0.f ? inv : rep) : z;
+  __device__ __forceinline__ float operator()(float z, bool seen, uint32_t n) const {
+    const float y = seen ? z * (z > 0.f ? inv : rep) : z;
     return n ? fmaf(-freq, (float)n, y) - pres : y;
   }
 };
 
-// Counts a token in shared memory if off < len. Predicated: a warp's 32 ids rarely miss a
-// slice all together, and a branch around every atomic costs more than the atomic.
-template <bool kOutput>
-__device__ __forceinline__ void count_token(uint32_t count, uint32_t off, uint32_t len) {
-  if (kOutput)
-    asm volatile("{ .reg .pred p; setp.lt.u32 p, %0, %1; @p red.shared.add.u32 [%2], 1; }" ::"r"(off), "r"(len),
-                 "r"(count + off * 4)
+// What the lists say of the tokens of a piece of the vocabulary, in shared memory: bits for
+// "in the prompt" and "has a bias", and the times in the output. 16 bits a token where the
+// output is short enough to be counted in 14 of them, else 32: pieces are twice as large
+// with 16, and the history is read once a piece.
+template <int kBits>
+struct Counts {
+  static constexpr uint32_t kPrompt = 1u << (kBits - 1), kBias = 1u << (kBits - 2), kTimes = kBias - 1;
+  static constexpr int kWords = kGroup * kBits / 32;  // of a group
+  uint32_t at;   // shared memory address of the entries
+  uint32_t pad;  // entries before token 0, so that groups are 16-byte aligned
+  __device__ __forceinline__ uint32_t address(uint32_t off) const {
+    return at + (kBits == 16 ? (off + pad) / 2 : off + pad) * 4;
+  }
+  __device__ __forceinline__ uint32_t shift(uint32_t off) const { return kBits == 16 ? (off + pad) % 2 * 16 : 0; }
+  // Adds to (or sets bits in) a token's entry if off < len. Predicated: a warp's 32 ids
+  // rarely miss a piece all together, and a branch around every atomic costs more.
+  __device__ __forceinline__ void add(uint32_t off, uint32_t len) const {
+    asm volatile("{ .reg .pred p; setp.lt.u32 p, %0, %1; @p red.shared.add.u32 [%2], %3; }" ::"r"(off), "r"(len),
+                 "r"(address(off)), "r"(1u << shift(off))
                  : "memory");
-  else
+  }
+  __device__ __forceinline__ void set(uint32_t off, uint32_t len, uint32_t bits) const {
     asm volatile("{ .reg .pred p; setp.lt.u32 p, %0, %1; @p red.shared.or.b32 [%2], %3; }" ::"r"(off), "r"(len),
-                 "r"(count + off * 4), "r"(kPromptBit)
+                 "r"(address(off)), "r"(bits << shift(off))
                  : "memory");
-}
+  }
+  __device__ __forceinline__ uint32_t word(uint32_t off) const {
+    uint32_t w;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(address(off)) : "memory");
+    return w;
+  }
+  __device__ __forceinline__ uint32_t get(uint32_t off) const {
+    return kBits == 16 ? word(off) >> shift(off) & 0xffffu : word(off);
+  }
+  // A group's words; token k of them.
+  __device__ __forceinline__ void group(uint32_t off, uint32_t (&w)[kWords]) const {
+#pragma unroll
+    for (int i = 0; i < kWords; i += 4)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                   : "r"(address(off) + i * 4)
+                   : "memory");
+  }
+  __device__ __forceinline__ static uint32_t of(const uint32_t (&w)[kWords], int k) {
+    return kBits == 16 ? (k & 1 ? w[k / 2] >> 16 : w[k / 2] & 0xffffu) : w[k];
+  }
+};
 
-// Counts a request's tokens [v0, v0 + len) at count[v - v0], from `pn` prompt and `on`
-// output ids; returns whether an id is outside the vocabulary. An id is compared by its
-// halves: the high one has to be 0. The loads of both lists' last pieces (most lists are
-// no longer) go out together.
+// Counts the tokens [v0, v0 + len) among `pn` prompt and `on` output ids; returns whether
+// an id is outside the vocabulary. An id is compared by its halves: the high one has to be
+// 0. The loads of both lists' last pieces (most lists are no longer) go out together.
+template <int kBits>
 __device__ __forceinline__ bool count_ids(const int64_t* p_ids, int32_t pn, const int64_t* o_ids, int32_t on, uint32_t V,
-                                          uint32_t v0, uint32_t len, uint32_t count) {
+                                          uint32_t v0, uint32_t len, const Counts<kBits>& counts) {
   constexpr int kAhead = 8;  // ids of a list in flight
   constexpr int32_t kRound = kLogitThreads * kAhead;
   uint32_t high = 0, most = 0;  // over all ids
@@ -100,9 +132,9 @@ __device__ __forceinline__ bool count_ids(const int64_t* p_ids, int32_t pn, cons
     most = max(most, id.x);
     const uint32_t off = id.y ? 0xffffffffu : id.x - v0;
     if (output)
-      count_token<true>(count, off, len);
+      counts.add(off, len);
     else
-      count_token<false>(count, off, len);
+      counts.set(off, len, Counts<kBits>::kPrompt);
   };
   const uint2* p = reinterpret_cast<const uint2*>(p_ids) + threadIdx.x;
   const uint2* o = reinterpret_cast<const uint2*>(o_ids) + threadIdx.x;
@@ -131,17 +163,19 @@ __device__ __forceinline__ bool count_ids(const int64_t* p_ids, int32_t pn, cons
   return high != 0 || most >= V;
 }
 
-template <typename in_t, typename out_t, bool kLists>
-__global__ void __launch_bounds__(kLogitThreads, kLogitBlocks) k_logits(LogitsArgs a) {
-  extern __shared__ __align__(16) uint32_t smem[];
-  __shared__ int repeated;  // a bias list names a token twice
-  pdl_wait();
-  pdl_trigger();
-  const int32_t b = blockIdx.y;
-  const int32_t v0 = (int32_t)blockIdx.x * a.slice, len = min(a.V - v0, a.slice);
+// A request's lists: [start, end) in each.
+struct Lists {
+  int64_t ps, pe, os, oe, bs, be;
+};
+
+// Tokens [v0, v0 + len) of request b. kBits 0: there are no lists.
+template <typename in_t, typename out_t, int kBits>
+__device__ __forceinline__ void process(const LogitsArgs& a, int32_t b, int32_t v0, int32_t len, const Lists& l,
+                                        const Penalty& penalty, uint32_t* smem, int* repeated) {
+  using C = Counts<kBits ? kBits : 32>;
   const in_t* z = static_cast<const in_t*>(a.z) + b * a.z_stride + v0;
   out_t* y = static_cast<out_t*>(a.y) + b * a.y_stride + v0;
-  // Groups of eight start `head` tokens into the slice, so that stores are 16-byte
+  // Groups of eight start `head` tokens into the piece, so that stores are 16-byte
   // aligned, and loads too where input and output allow it together.
   constexpr uint32_t in_n = 16 / sizeof(in_t), out_n = 16 / sizeof(out_t), both_n = in_n < out_n ? in_n : out_n;
   const uint32_t in_at = (uint32_t)(reinterpret_cast<uintptr_t>(z) / sizeof(in_t)) % in_n;
@@ -149,17 +183,10 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitBlocks) k_logits(LogitsAr
   const bool wide_loads = in_at % both_n == out_at % both_n;
   const int32_t head = min(len, (int32_t)(wide_loads && in_n > out_n ? -in_at % in_n : -out_at % out_n));
   const int32_t groups = (len - head) / kGroup;
-  uint32_t* count = smem + (-head & 3);  // groups' counts are 16-byte aligned
+  const C counts{smem_u32(smem), (uint32_t)(-head & 7)};
   const uint32_t* mask = a.mask ? a.mask + b * a.mask_stride : nullptr;
-  const float rep = a.rep ? a.rep[b] : 1.f;
-  const Penalty penalty{rep, __frcp_rn(rep), a.freq ? a.freq[b] : 0.f, a.pres ? a.pres[b] : 0.f};
-  int64_t ps = 0, pe = 0, os = 0, oe = 0, bs = 0, be = 0;
-  if (kLists) {
-    if (a.p_ids) list_of(a.p_off, a.p_n, b, a.status, &ps, &pe);
-    if (a.o_ids) list_of(a.o_off, a.o_n, b, a.status, &os, &oe);
-    if (a.b_ids) list_of(a.b_off, a.b_n, b, a.status, &bs, &be);
-  }
   auto allowed = [&](uint32_t v) { return !mask || (mask[v >> 5] >> (v & 31) & 1u); };
+  auto penalised = [&](float x, uint32_t c) { return penalty(x, c & ~C::kBias, c & C::kTimes); };
   // kBatch groups a thread are in flight; the first go out before the lists are read.
   const in_t* zg = z + head;
   out_t* yg = y + head;
@@ -179,21 +206,26 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitBlocks) k_logits(LogitsAr
   // a thread's first bias: its token, logit and value, ahead of their use
   int64_t own_id = -1;
   float own_z = 0.f, own_bias = 0.f;
-  if (kLists && bs + threadIdx.x < be) {
-    own_id = a.b_ids[bs + threadIdx.x];
-    own_bias = a.b_val[bs + threadIdx.x];
+  if (kBits && l.bs + threadIdx.x < l.be) {
+    own_id = a.b_ids[l.bs + threadIdx.x];
+    own_bias = a.b_val[l.bs + threadIdx.x];
   }
-  if (kLists) {
+  if (kBits) {
     uint4* c4 = reinterpret_cast<uint4*>(smem);
-    for (int32_t i = threadIdx.x; i < a.slice / 4 + 1; i += kLogitThreads) c4[i] = make_uint4(0, 0, 0, 0);
-    if (threadIdx.x == 0) repeated = 0;
+    for (int32_t i = threadIdx.x; i < (len + kGroup) * C::kWords / (4 * kGroup) + 1; i += kLogitThreads)
+      c4[i] = make_uint4(0, 0, 0, 0);
+    if (threadIdx.x == 0) *repeated = 0;
     __syncthreads();
-    bool bad = count_ids(a.p_ids + ps, (int32_t)(pe - ps), a.o_ids + os, (int32_t)(oe - os), a.V, v0, len,
-                         smem_u32(count));
-    for (int64_t j = bs + threadIdx.x; j < be; j += kLogitThreads) {
-      const int64_t v = j == bs + threadIdx.x ? own_id : a.b_ids[j];
+    bool bad = count_ids(a.p_ids + l.ps, (int32_t)(l.pe - l.ps), a.o_ids + l.os, (int32_t)(l.oe - l.os), a.V, v0, len,
+                         counts);
+    for (int64_t j = l.bs + threadIdx.x; j < l.be; j += kLogitThreads) {
+      const int64_t v = j == l.bs + threadIdx.x ? own_id : a.b_ids[j];
       bad |= v < 0 || v >= a.V;
-      if (v >= v0 && v < v0 + len && (atomicOr(&count[v - v0], kBiasBit) & kBiasBit)) repeated = 1;
+      if (v < v0 || v >= v0 + len) continue;
+      const uint32_t off = (uint32_t)(v - v0), bit = C::kBias << counts.shift(off);
+      uint32_t old;
+      asm volatile("atom.shared.or.b32 %0, [%1], %2;" : "=r"(old) : "r"(counts.address(off)), "r"(bit) : "memory");
+      if (old & bit) *repeated = 1;
     }
     if (bad) report(a.status, kErrIndex);
     if (own_id >= v0 && own_id < v0 + len) own_z = Elem<in_t>::get(z[own_id - v0]);
@@ -214,14 +246,14 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitBlocks) k_logits(LogitsAr
       const uint32_t keep = mask ? __funnelshift_r(words[u].x, words[u].y, v0 + head + i * kGroup) : ~0u;
       load(u, i + kBatch * kLogitThreads);
       uint32_t any = 0;
-      if (kLists) {
-        const uint4* c4 = reinterpret_cast<const uint4*>(count + head + i * kGroup);
-        const uint4 lo = c4[0], hi = c4[1];
-        any = lo.x | lo.y | lo.z | lo.w | hi.x | hi.y | hi.z | hi.w;
-        if (any) {
-          const uint32_t c[kGroup] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      if (kBits) {
+        uint32_t w[C::kWords];
+        counts.group(head + i * kGroup, w);
 #pragma unroll
-          for (int k = 0; k < kGroup; ++k) x[k] = penalty(x[k], c[k]);
+        for (int k = 0; k < C::kWords; ++k) any |= w[k];
+        if (any) {
+#pragma unroll
+          for (int k = 0; k < kGroup; ++k) x[k] = penalised(x[k], C::of(w, k));
         }
       }
       if (mask) {
@@ -229,35 +261,72 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitBlocks) k_logits(LogitsAr
         for (int k = 0; k < kGroup; ++k)
           if (!(keep >> k & 1u)) x[k] = -INFINITY;
       }
-      if (!(any & kBiasBit)) {
+      if (!(any & (kBits == 16 ? C::kBias * 0x10001u : C::kBias))) {
         store8(yg + i * kGroup, x);
       } else {
 #pragma unroll
         for (int k = 0; k < kGroup; ++k)
-          if (!(count[head + i * kGroup + k] & kBiasBit)) yg[i * kGroup + k] = Elem<out_t>::put(x[k]);
+          if (!(counts.get(head + i * kGroup + k) & C::kBias)) yg[i * kGroup + k] = Elem<out_t>::put(x[k]);
       }
     }
   }
   // the few tokens before the first group and after the last
   for (int32_t o = threadIdx.x; o < len - groups * kGroup; o += kLogitThreads) {
     const int32_t at = o < head ? o : o + groups * kGroup;
-    const uint32_t c = kLists ? count[at] : 0;
-    if (!(c & kBiasBit)) y[at] = Elem<out_t>::put(allowed(v0 + at) ? penalty(Elem<in_t>::get(z[at]), c) : -INFINITY);
+    const uint32_t c = kBits ? counts.get(at) : 0;
+    if (!(c & C::kBias)) y[at] = Elem<out_t>::put(allowed(v0 + at) ? penalised(Elem<in_t>::get(z[at]), c) : -INFINITY);
   }
   // Each biased token by the thread of its first entry; its biases in list order.
-  for (int64_t j = bs + threadIdx.x; j < be; j += kLogitThreads) {
-    const bool first = j == bs + threadIdx.x;
+  for (int64_t j = l.bs + threadIdx.x; kBits && j < l.be; j += kLogitThreads) {
+    const bool first = j == l.bs + threadIdx.x;
     const int64_t v = first ? own_id : a.b_ids[j];
     if (v < v0 || v >= v0 + len) continue;
     bool mine = true;
-    if (repeated)
-      for (int64_t i = bs; i < j && mine; ++i) mine = a.b_ids[i] != v;
+    if (*repeated)
+      for (int64_t i = l.bs; i < j && mine; ++i) mine = a.b_ids[i] != v;
     if (!mine) continue;
-    float x = penalty(first ? own_z : Elem<in_t>::get(z[v - v0]), count[v - v0]) + (first ? own_bias : a.b_val[j]);
-    if (repeated)
-      for (int64_t i = j + 1; i < be; ++i)
+    float x = penalised(first ? own_z : Elem<in_t>::get(z[v - v0]), counts.get((uint32_t)(v - v0))) +
+              (first ? own_bias : a.b_val[j]);
+    if (*repeated)
+      for (int64_t i = j + 1; i < l.be; ++i)
         if (a.b_ids[i] == v) x += a.b_val[i];
     y[v - v0] = Elem<out_t>::put(allowed((uint32_t)v) ? x : -INFINITY);
+  }
+}
+
+// Apart from the usual ones, so that they share no registers with these.
+template <typename in_t, typename out_t>
+__device__ __noinline__ void process_long(const LogitsArgs& a, int32_t b, int32_t v0, int32_t len, const Lists& l,
+                                          const Penalty& penalty, uint32_t* smem, int* repeated) {
+  process<in_t, out_t, 32>(a, b, v0, len, l, penalty, smem, repeated);
+}
+
+template <typename in_t, typename out_t, bool kLists>
+__global__ void __launch_bounds__(kLogitThreads, kLogitBlocks) k_logits(LogitsArgs a) {
+  extern __shared__ __align__(16) uint32_t smem[];
+  __shared__ int repeated;  // a bias list names a token twice
+  pdl_wait();
+  pdl_trigger();
+  const int32_t b = blockIdx.y;
+  const int32_t v0 = (int32_t)blockIdx.x * a.slice, len = min(a.V - v0, a.slice);
+  const float rep = a.rep ? a.rep[b] : 1.f;
+  const Penalty penalty{rep, __frcp_rn(rep), a.freq ? a.freq[b] : 0.f, a.pres ? a.pres[b] : 0.f};
+  Lists l{};
+  if constexpr (!kLists) {
+    process<in_t, out_t, 0>(a, b, v0, len, l, penalty, smem, &repeated);
+    return;
+  }
+  if (a.p_ids) list_of(a.p_off, a.p_n, b, a.status, &l.ps, &l.pe);
+  if (a.o_ids) list_of(a.o_off, a.o_n, b, a.status, &l.os, &l.oe);
+  if (a.b_ids) list_of(a.b_off, a.b_n, b, a.status, &l.bs, &l.be);
+  if (l.oe - l.os <= (int64_t)Counts<16>::kTimes) {
+    process<in_t, out_t, 16>(a, b, v0, len, l, penalty, smem, &repeated);
+    return;
+  }
+  const int32_t half = a.slice / 2;  // the room of a slice's 16-bit entries
+  for (int32_t o = 0; o < len; o += half) {
+    __syncthreads();  // the piece before is done with its counts
+    process_long<in_t, out_t>(a, b, v0 + o, min(half, len - o), l, penalty, smem, &repeated);
   }
 }
 
@@ -276,9 +345,9 @@ cudaError_t launch(int device, LogitsArgs& a, cudaStream_t s) {
                          args, true);
   const void* fn = reinterpret_cast<const void*>(&k_logits<in_t, out_t, true>);
   static bool ready[64];
-  const cudaError_t e = allow_smem(fn, (kMaxSlice + 4) * 4, device, ready);
+  const cudaError_t e = allow_smem(fn, kMaxSlice * 2 + 128, device, ready);
   if (e != cudaSuccess) return e;
-  return launch_kernel(fn, grid, dim3(kLogitThreads), (a.slice + 4) * 4, s, args, true);
+  return launch_kernel(fn, grid, dim3(kLogitThreads), (size_t)a.slice * 2 + 128, s, args, true);
 }
 
 template <typename in_t>

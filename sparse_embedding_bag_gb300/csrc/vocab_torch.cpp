@@ -135,6 +135,8 @@ PyObject* entry(Py_ssize_t given, Py_ssize_t wanted, F body) {
   } catch (const Refused&) {
   } catch (const std::exception& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {
+    PyErr_SetString(PyExc_RuntimeError, "unknown C++ exception");
   }
   return nullptr;
 }
