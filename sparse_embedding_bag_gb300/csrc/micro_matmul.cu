@@ -131,6 +131,12 @@ __global__ void __launch_bounds__(kMatmulThreads, 1)
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, ctl.tmem, 0);
   pdl_trigger();
+  // The first rows of the table start towards L2 while the kernel before ends (it may write
+  // them: what L2 holds is then written there).
+  if (warp == 4 && lane == 0 && x_tiles == 1 && first < tiles)
+    for (int32_t k = 0; k < min(k_stages, (int32_t)S::kStages); ++k)
+      tensor_prefetch(&wmap, k * 128, (int32_t)(first * S::kCtas + rank) * kRows);
+  __syncwarp();
   pdl_wait();  // operands may come from the kernel before; it may still read the output's buffer
 
   if (warp == 4 && lane == 0) {

@@ -154,6 +154,11 @@ __device__ __forceinline__ void tensor_load(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+// Brings a box to L2.
+__device__ __forceinline__ void tensor_prefetch(const CUtensorMap* map, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
+}
+
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
