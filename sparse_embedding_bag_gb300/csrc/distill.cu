@@ -345,7 +345,6 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks) k_distill_rows(DistillAr
   const T* z = static_cast<const T*>(a.z) + n * a.z_stride + r0;
   T* dz = kGrad ? static_cast<T*>(a.dz) + n * a.dz_stride + r0 : nullptr;
   pdl_wait();
-  pdl_trigger();
   const Cut<T> cut(z, len);  // the order of the sums goes by the logits' alignment alone
   uint4 raw[kBatch];
   load_first<true>(z, cut, raw);

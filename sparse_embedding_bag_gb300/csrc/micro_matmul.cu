@@ -130,9 +130,9 @@ __global__ void __launch_bounds__(kMatmulThreads, 1)
     __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, ctl.tmem, 0);
-  pdl_trigger();
   // The first rows of the table start towards L2 while the kernel before ends (it may write
-  // them: what L2 holds is then written there).
+  // them: what L2 holds is then written there). The kernel after is not let in early: its
+  // waiting blocks beside these cost 2 us of 22 at 97 tokens x 50001 x 2056.
   if (warp == 4 && lane == 0 && x_tiles == 1 && first < tiles)
     for (int32_t k = 0; k < min(k_stages, (int32_t)S::kStages); ++k)
       tensor_prefetch(&wmap, k * 128, (int32_t)(first * S::kCtas + rank) * kRows);
