@@ -24,7 +24,7 @@
 // still in L2 (all rows under way are a third of it), so HBM sees one read and one write.
 // Backward (its sums are known): blocks over pieces of the rows, one read and one write.
 // Holding the rows in shared memory instead (bulk copies, three CTAs of 64 KB an SM) took
-// 474 us a step at 4096 x 128256 bf16, against 393: a CTA does nothing else while its
+// 474 us a step at 4096 x 128256 bf16, against 395: a CTA does nothing else while its
 // slice arrives, and reads it three times.
 #include <cmath>
 
