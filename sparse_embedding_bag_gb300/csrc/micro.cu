@@ -3,8 +3,8 @@
 // Both are bound by HBM traffic. A thread takes units of 8 elements, so that a warp's codes
 // are whole 128-byte lines and its 16-bit values whole 512-byte ones; a team of lanes (a
 // warp, or less for short rows) takes a piece of a row, kBatch loads of each lane in flight.
-// Measured at 128256 x 4096 (HBM bytes over time): bf16 to MX 221 us, 6.0 TB/s, to NV 265 us;
-// fp32 to MX 334 us, 7.1 TB/s; MX or NV to bf16 208 us, 6.4 TB/s, to fp32 438 us, 5.4 TB/s.
+// Measured at 128256 x 4096 (HBM bytes over time): bf16 to MX 219 us, 6.1 TB/s, to NV 270 us;
+// fp32 to MX 326 us, 7.3 TB/s; MX or NV to bf16 208 us, 6.4 TB/s, to fp32 425 us, 5.6 TB/s.
 // 16-bit types are nearly bound by instructions (the conversions run at a quarter of the
 // rate): checking every unit's place in its row took 10 % more.
 #include <cmath>
@@ -41,9 +41,9 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&x)[kGroup]) {
   return r;
 }
 
-// Rows and blocks are taken up to whole scale tiles, whose padding is zero. Rows that do not
-// start at 16 bytes are read element by element from L1 (128256 x 4096 bf16 to MX: 454 us
-// against 221); reading the aligned pieces that cover them and shifting took 555 us.
+// Rows and blocks are taken up to whole scale tiles, whose padding is zero. 16-bit rows that
+// do not start at 16 bytes are read by words (128256 x 4096 bf16 to MX: 297 us against 219;
+// element by element 454, shifting aligned 16-byte pieces 555), fp32 ones by elements.
 template <typename T, int kFormat>
 __global__ void __launch_bounds__(kThreads) k_micro_quantize(QuantArgs a, int log_team) {
   constexpr int n = micro_block(kFormat), lanes = n / kGroup;  // lanes of a block
@@ -58,11 +58,22 @@ __global__ void __launch_bounds__(kThreads) k_micro_quantize(QuantArgs a, int lo
   const bool row = r < a.R, wide = row && reinterpret_cast<uintptr_t>(x) % 16 == 0;
   // Are all of this team's units whole and loaded 16 bytes at a time? Then nothing is checked.
   const bool plain = wide && ((int32_t)blockIdx.y + 1) * kBatch * team * kGroup <= a.K;
+  // Units of 16-bit rows elsewhere come in the four or (rows at odd elements) five words that
+  // cover them, where these lie in the row.
+  const int32_t odd = sizeof(T) == 2 ? (int32_t)(reinterpret_cast<uintptr_t>(x) / 2 % 2) : 0;
+  auto in_words = [&](int32_t k) { return sizeof(T) == 2 && row && !wide && k >= odd && k + kGroup + odd <= a.K; };
   Raw8<T> raw[kBatch];
+  uint32_t fifth[kBatch];
 #pragma unroll
   for (int b = 0; b < kBatch; ++b) {
     const int32_t k = (u0 + b * team) * kGroup;
-    if (plain || (wide && k + kGroup <= a.K)) raw[b].load(x + k);
+    if (plain || (wide && k + kGroup <= a.K)) {
+      raw[b].load(x + k);
+    } else if (in_words(k)) {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(x + k - odd);
+      raw[b].u[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      fifth[b] = odd ? w[4] : 0;
+    }
   }
   uint8_t* codes = a.codes + r * row_bytes + u0 * 4;
   uint8_t* word_at = a.scales + micro_scale_at(r, u0 / lanes, tiles);
@@ -71,6 +82,12 @@ __global__ void __launch_bounds__(kThreads) k_micro_quantize(QuantArgs a, int lo
     const int32_t u = u0 + b * team, k = u * kGroup;
     float v[kGroup];
     if (!checked || (wide && k + kGroup <= a.K)) {
+      raw[b].widen(v);
+    } else if (in_words(k)) {
+      uint4& w = raw[b].u[0];
+      if (odd)
+        w = make_uint4(__funnelshift_r(w.x, w.y, 16), __funnelshift_r(w.y, w.z, 16), __funnelshift_r(w.z, w.w, 16),
+                       __funnelshift_r(w.w, fifth[b], 16));
       raw[b].widen(v);
     } else {
 #pragma unroll
