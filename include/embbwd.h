@@ -407,7 +407,7 @@ emb_status emb_logits_process(int device, const void* logits, emb_dtype logits_d
  *   emb_distill_backward  dlogits (logits_dtype) = row_weight[n] * dloss/dz from the
  *                         forward's stats; row_weight fp32[N] or NULL = 1
  *   emb_distill_step      loss and dlogits in one call, for a row_weight known
- *                         beforehand; z is read once where a row fits on chip
+ *                         beforehand; z is read from HBM once
  * dlogits may be logits itself (same stride) and must not overlap it otherwise. */
 emb_status emb_distill_forward(int device, const void* logits, emb_dtype logits_dtype,
                                int64_t logits_stride, int32_t N, int32_t V,

@@ -330,7 +330,7 @@ def test_distill_reports_bad_ids(V):
 
 
 def test_distill_wide_rows(V):
-    # rows wider than a cluster's shared memory holds
+    # the widest rows
     rng = np.random.default_rng(8)
     N, n_vocab, K = 2, 1 << 20, 16
     ids, t = teacher_lists(rng, N, n_vocab, K)
