@@ -401,9 +401,12 @@ emb_status emb_logits_process(int device, const void* logits, emb_dtype logits_d
  *   d loss / d z_v = tau * (p_v - q of the entries with id v)   on the list,
  *                    tau * p_v * (1 - r / u)                    off it.
  * Entries with id -1 are padding. Rows without entries, and rows with L = -infinity (a
- * teacher without mass), have loss 0 and gradient 0. Entries that repeat an id add.
+ * teacher without mass), have loss 0 and gradient 0. Entries that repeat an id add. Where no
+ * logit off the list is finite (u = 0), an r within rounding of 0 counts as 0; a larger one
+ * makes the loss infinite, and the gradient off the list is 0.
  *   emb_distill_forward   loss fp32[N]; stats fp32[N, 4], 16-byte aligned: {largest z,
- *                         sum of exp((z - largest) / tau), 1 - r / u, L}
+ *                         sum of exp((z - largest) / tau), 1 - r / u, L}; for r / u above
+ *                         2^64 its binary logarithm stands in place of 1 - r / u
  *   emb_distill_backward  dlogits (logits_dtype) = row_weight[n] * dloss/dz from the
  *                         forward's stats; row_weight fp32[N] or NULL = 1
  *   emb_distill_step      loss and dlogits in one call, for a row_weight known

@@ -9,9 +9,13 @@
 //   dloss/dz_v = tau [ p_v - sum_{k: id_k = v} q_k ]   for v on the list,
 //                tau p_v (1 - r / u)                   off it.
 // u is summed over the tokens off the list, never as 1 - (mass on it): it would
-// cancel for a student that agrees with its teacher. Entries with id -1 are
+// cancel for a student that agrees with its teacher. The sum is relative to a
+// reference near the largest logit off the list: relative to the row's largest, which is
+// usually a listed one, it underflows once the listed tokens lead by 87 tau. Entries with id -1 are
 // padding; a row without entries, or whose teacher has no mass (L = -infinity), has
-// loss 0 and gradient 0.
+// loss 0 and gradient 0. With no finite logit off the list u is 0: an r that rounding
+// explains counts as 0, a larger one makes the loss infinite; either way the gradient
+// off the list is 0.
 //
 // Exponentials are base 2: 2^((z_v - ref) c), c = log2(e) / tau. Differences come first, so
 // that rows masked with the type's lowest value neither overflow nor lose their maximum.
@@ -153,10 +157,35 @@ __device__ __forceinline__ float loss_of(const DistillArgs& a, int32_t n, const 
     }
   return block_all<false>(ls, scratch);
 }
-__device__ __forceinline__ float tail_of(float qsum, float rest, float S, float* coef) {
-  const float r = fmaxf(0.f, 1.f - qsum), u = rest / S;
-  *coef = r > 0.f ? 1.f - r / u : 1.f;
-  return r > 0.f ? r * (logf(r) - logf(u)) : 0.f;
+
+// 2^((a - b) c), 1 for equal ones (infinities among them).
+__device__ __forceinline__ float power_of(float a, float b, float c2) { return a == b ? 1.f : ex2((a - b) * c2); }
+
+// r / u above 2^kLargeRatio is held by its binary logarithm: a coefficient above 1.
+constexpr float kLargeRatio = 64.f;
+
+// The remaining mass's part of the loss (without tau^2), and the coefficient off the list.
+// `off` is the sum there relative to `ref`.
+__device__ __forceinline__ float tail_of(const DistillArgs& a, float qsum, float L, float off, float ref, float S,
+                                         float M, float* coef) {
+  const float r = fmaxf(0.f, 1.f - qsum);
+  *coef = 1.f;
+  // Each q carries a few roundings of values up to |L| + |log q|, L the caller's as many.
+  if (off == 0.f) return r > 0x1p-24f * (8.f * fabsf(L) + (float)a.K + 32.f) ? INFINITY : 0.f;
+  if (!(r > 0.f)) return 0.f;
+  const float ratio = logf(r) - (__fmul_rn(ref - M, a.inv_tau) + (logf(off) - logf(S)));  // log(r / u)
+  const float lg = ratio * 1.44269504f;
+  *coef = lg > kLargeRatio ? lg : 1.f - r / (off * power_of(ref, M, a.c2) / S);
+  return r * ratio;
+}
+
+// The gradient off the list is g 2^((z - ref) c): (scale / S) coef 2^((z - M) c). The exponent
+// takes up a coefficient far below 0, so that no power underflows whose product with it
+// does not.
+__device__ __forceinline__ void off_list(const DistillArgs& a, float coef, float scale, float M, float S, float* ref,
+                                         float* g) {
+  *ref = M, *g = scale * coef / S;
+  if (coef > 1.f || coef < -65536.f) *ref = M - (coef > 1.f ? coef : log2f(-coef)) / a.c2, *g = -scale / S;
 }
 
 // 16 bytes of a row, as pairs of floats.
@@ -283,24 +312,24 @@ __device__ __forceinline__ void load_first(const T* z, const Cut<T>& cut, uint4 
       raw[k] = cut.template load<kWide>(z, threadIdx.x + k * kThreads);
 }
 
-// The gradient of a part of a row off the list: g 2^(..), g = weight tau coefficient / S.
+// The gradient of a part of a row off the list: g 2^((z - ref) c).
 template <bool kWide, typename T>
 __device__ __forceinline__ void store_gradient(const T* z, T* dz, int32_t len, const Cut<T>& cut, uint4 (&raw)[kBatch],
-                                               float c, float M, float g) {
+                                               float c, float ref, float g) {
   using U = Unit<T>;
-  const F2 g2 = F2::of(g, g), c2 = F2::of(c, c), minus_M = F2::of(-M, -M);
+  const F2 g2 = F2::of(g, g), c2 = F2::of(c, c), minus_ref = F2::of(-ref, -ref);
   uint4* out = reinterpret_cast<uint4*>(dz + cut.head);
   for_units<kWide>(z, cut, raw, [&](int32_t u, const F2 (&x)[U::n / 2], float) {
     F2 e[U::n / 2];
     float2 w[U::n / 2];
-    powers(x, minus_M, c2, e);
+    powers(x, minus_ref, c2, e);
 #pragma unroll
     for (int i = 0; i < U::n / 2; ++i) w[i] = (e[i] * g2).get();
     out[u] = U::narrow(w);
   });
   for (int32_t o = threadIdx.x; o < len - cut.units * U::n; o += kThreads) {
     const int32_t e = cut.beside(o);
-    dz[e] = Elem<T>::put(g * ex2((Elem<T>::get(z[e]) - M) * c));
+    dz[e] = Elem<T>::put(g * ex2((Elem<T>::get(z[e]) - ref) * c));
   }
 }
 template <typename T>
@@ -337,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks) k_distill_rows(DistillAr
   extern __shared__ __align__(16) uint32_t bitmap[];  // of the part; then the list
   __shared__ List l;
   __shared__ float scratch[64];
-  __shared__ float parts[3][kMaxCluster];  // of every CTA: largest logit, sums off and on the list
+  __shared__ float4 parts[kMaxCluster];  // of every CTA: largest logit, reference off the list, sums off and on it
   cluster_arrive();  // shared memory of a CTA is written by others only once it runs
   const uint32_t ctas = 1u << log_ctas, rank = blockIdx.x & (ctas - 1);
   const int32_t n = blockIdx.x >> log_ctas;
@@ -375,14 +404,13 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks) k_distill_rows(DistillAr
   mark_list(a, l, bitmap, r0, len, first);
   __syncthreads();
   // This thread's largest logit, and its sum off the list relative to a reference that is
-  // raised when a value exceeds it by a factor of 2^kSlack.
+  // raised when a value there exceeds it by a factor of 2^kSlack.
   constexpr float kSlack = 16.f;
   const float slack = kSlack / a.c2;
   float m = -INFINITY, ref = -3.402823466e38f;
   const F2 c2 = F2::of(a.c2, a.c2);
   F2 sum = F2::of(0.f, 0.f);
   auto raise = [&](float most) {
-    m = fmaxf(m, most);
     if (most > ref + slack) {
       const float f = ex2((ref - most) * a.c2);
       sum = sum * F2::of(f, f);
@@ -391,16 +419,26 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks) k_distill_rows(DistillAr
   };
   const uint8_t* on_list = reinterpret_cast<const uint8_t*>(bitmap) + 1;
   for_units<true>(z, cut, raw, [&](int32_t u, F2 (&x)[U::n / 2], float most) {
-    raise(most);
+    m = fmaxf(m, most);
     F2 e[U::n / 2];
     const uint32_t bits = U::n == 8 ? on_list[u] : on_list[u >> 1] >> (u & 1) * 4 & 15u;
-    if (bits) {
+    auto mask = [&] {
 #pragma unroll
       for (int i = 0; i < U::n / 2; ++i) {
         const float2 y = x[i].get();
         x[i] = F2::of(bits >> 2 * i & 1u ? -INFINITY : y.x, bits >> 2 * i & 2u ? -INFINITY : y.y);
       }
+    };
+    if (most > ref + slack) {
+      if (bits) {
+        mask();
+        most = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < U::n / 2; ++i) most = fmaxf(most, fmaxf(x[i].get().x, x[i].get().y));
+      }
+      raise(most);
     }
+    if (bits) mask();
     powers(x, F2::of(-ref, -ref), c2, e);
 #pragma unroll
     for (int i = 0; i < U::n / 2; ++i) sum = sum + e[i];
@@ -408,42 +446,50 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks) k_distill_rows(DistillAr
   for (int32_t o = threadIdx.x; o < len - cut.units * U::n; o += kThreads) {
     const int32_t e = cut.beside(o);
     const float x = Elem<T>::get(z[e]);
+    m = fmaxf(m, x);
+    if (bitmap[(e + first) >> 5] >> ((e + first) & 31) & 1u) continue;
     raise(x);
-    if (!(bitmap[(e + first) >> 5] >> ((e + first) & 31) & 1u)) sum = sum + F2::of(ex2((x - ref) * a.c2), 0.f);
+    sum = sum + F2::of(ex2((x - ref) * a.c2), 0.f);
   }
   const Cut<T> again(kGrad ? dz : z, len);
   if (kGrad) load_first<kWide>(z, again, raw);
-  // relative to the part's largest logit; with nothing but -infinity there is no sum
-  float M = block_all<true>(m, scratch);
-  float rest = sum.get().x + sum.get().y, top = 0.f;
+  // the part's largest logit and reference, and its sums relative to them (with nothing but
+  // -infinity there is none)
+  float rest = sum.get().x + sum.get().y, top = 0.f, M = m, R = ref;
+  block_both<true>(M, R, scratch);
+  rest *= power_of(ref, R, a.c2);
   const float base = M == -INFINITY ? 0.f : M;
-  rest *= ref == base ? 1.f : ex2((ref - base) * a.c2);
   for (int k = threadIdx.x; k < a.K; k += kThreads) {
     const int32_t e = l.id[k] - r0;
     if (l.id[k] >= 0 && e >= 0 && e < len && is_first(l, k)) top += ex2((l.z[k] - base) * a.c2);
   }
-  block_sums(rest, top, scratch);
+  block_both<false>(rest, top, scratch);
   __syncwarp();
   cluster_wait();
-  if (threadIdx.x < ctas) {
-    cluster_store(cluster_map(smem_u32(&parts[0][rank]), threadIdx.x), M);
-    cluster_store(cluster_map(smem_u32(&parts[1][rank]), threadIdx.x), rest);
-    cluster_store(cluster_map(smem_u32(&parts[2][rank]), threadIdx.x), top);
-  }
+  if (threadIdx.x < ctas)
+    cluster_store(cluster_map(smem_u32(&parts[rank]), threadIdx.x), make_float4(M, R, rest, top));
   __syncwarp();
   cluster_sync();
-  float S = 0.f, off = 0.f;
-  for (uint32_t i = 0; i < ctas; ++i) M = fmaxf(M, parts[0][i]);
-  for (uint32_t i = 0; i < ctas; ++i) {
-    const float f = parts[0][i] == M ? 1.f : ex2((parts[0][i] - M) * a.c2);
-    off += parts[1][i] * f;
-    S += parts[2][i] * f;
-  }
-  S += off;
+  // a lane a part, the same in every group of kMaxCluster lanes
+  const uint32_t part_of = threadIdx.x % kMaxCluster;
+  const float4 of_part = part_of < ctas ? parts[part_of] : make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+  M = of_part.x, R = of_part.y;
+#pragma unroll
+  for (int o = 1; o < kMaxCluster; o *= 2)
+    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o)), R = fmaxf(R, __shfl_xor_sync(0xffffffffu, R, o));
+  float off = of_part.z * power_of(of_part.y, R, a.c2), S = of_part.w * power_of(of_part.x, M, a.c2);
+#pragma unroll
+  for (int o = 1; o < kMaxCluster; o *= 2)
+    off += __shfl_xor_sync(0xffffffffu, off, o), S += __shfl_xor_sync(0xffffffffu, S, o);
+  S += off * power_of(R, M, a.c2);
   float coef = 1.f;
-  const float tail = a.lse ? tail_of(qsum, off, S, &coef) : 0.f;
+  const float tail = a.lse ? tail_of(a, qsum, L, off, R, S, M, &coef) : 0.f;
   const float scale = (a.weight ? a.weight[n] : 1.f) * a.tau;
-  if (kGrad) store_gradient<kWide>(z, dz, len, again, raw, a.c2, M, scale * coef / S);
+  if (kGrad) {
+    float off_ref, g;
+    off_list(a, coef, scale, M, S, &off_ref, &g);
+    store_gradient<kWide>(z, dz, len, again, raw, a.c2, off_ref, g);
+  }
   if (rank == 0) {
     const float loss = loss_of(a, n, l, scratch, M, S, L) + tail;
     if (threadIdx.x == 0) {
@@ -499,7 +545,9 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks) k_distill_backward(Disti
     store_zeros(dz, len, cut);
     return;
   }
-  store_gradient<kWide>(z, dz, len, cut, raw, a.c2, st.x, scale * st.z / st.y);
+  float ref, g;
+  off_list(a, st.z, scale, st.x, st.y, &ref, &g);
+  store_gradient<kWide>(z, dz, len, cut, raw, a.c2, ref, g);
   __syncthreads();
   store_listed(a, dz, l, scale, st.x, st.y);
 }

@@ -98,15 +98,17 @@ __device__ __forceinline__ float block_all(float v, float* scratch) {
   return kMax ? warp_max(v) : warp_sum(v);
 }
 
-// Both sums over a block; `scratch` holds 64 floats.
-__device__ __forceinline__ void block_sums(float& u, float& v, float* scratch) {
+// Both sums (maxima) over a block; `scratch` holds 64 floats.
+template <bool kMax>
+__device__ __forceinline__ void block_both(float& u, float& v, float* scratch) {
+  constexpr float none = kMax ? -INFINITY : 0.f;
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  u = warp_sum(u), v = warp_sum(v);
+  u = kMax ? warp_max(u) : warp_sum(u), v = kMax ? warp_max(v) : warp_sum(v);
   __syncthreads();
   if (lane == 0) scratch[warp] = u, scratch[32 + warp] = v;
   __syncthreads();
-  u = warp_sum(lane < warps ? scratch[lane] : 0.f);
-  v = warp_sum(lane < warps ? scratch[32 + lane] : 0.f);
+  u = lane < warps ? scratch[lane] : none, v = lane < warps ? scratch[32 + lane] : none;
+  u = kMax ? warp_max(u) : warp_sum(u), v = kMax ? warp_max(v) : warp_sum(v);
 }
 
 // ---- host side
