@@ -200,9 +200,13 @@ struct Rows {
   const float* of_rows(PyObject* o, int per_row, const char* name) const {
     return vector<float>(o, z.device, at::kFloat, (int64_t)N * per_row, name);
   }
-  // The gradient's tensor: `out`, or a new one with its rows as far apart as the logits'.
+  // The gradient's tensor: `out`, or a new one. Its rows are contiguous but for what puts them
+  // at the same places in 16 bytes as the logits' (a new tensor starts at such a boundary):
+  // then the kernels load whole pieces. The logits' own stride may be that of a whole sequence.
   Matrix gradient(PyObject* out) const {
-    const int64_t stride = std::max<int64_t>(z.stride, V);
+    const int64_t piece = 16 / (int64_t)z.t.element_size();
+    const bool alike = N > 1 && z.stride > V && reinterpret_cast<uintptr_t>(z.ptr()) % 16 == 0;
+    const int64_t stride = V + (alike ? (z.stride - V) % piece : 0);
     const Matrix g(out == Py_None ? at::empty_strided({N, V}, {stride, 1}, z.t.options()) : tensor(out, "out"), "out");
     g.wants(N, V, z.device, "out");
     if (g.dtype != z.dtype) refuse("out must have the type of logits");
