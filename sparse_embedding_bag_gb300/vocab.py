@@ -96,6 +96,7 @@ class _DistillLoss(torch.autograd.Function):
         return loss
 
     @staticmethod
+    @torch.autograd.function.once_differentiable  # the gradient's own derivatives are not built
     def backward(ctx, grad):
         logits, ids, teacher, stats = ctx.saved_tensors
         return (distill_backward(logits, ids, teacher, stats, grad.float().contiguous(),
@@ -103,7 +104,7 @@ class _DistillLoss(torch.autograd.Function):
 
 
 def distill_loss(logits, teacher_ids, teacher_logits, *, temperature=1.0, teacher_lse=None):
-    """Differentiable loss [N] of ``logits`` (the teacher takes no gradient)."""
+    """Differentiable loss [N] of ``logits`` (once; the teacher takes no gradient)."""
     return _DistillLoss.apply(logits, teacher_ids, teacher_logits, temperature, teacher_lse)
 
 
