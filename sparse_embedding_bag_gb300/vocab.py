@@ -86,6 +86,18 @@ def distill_step(logits, teacher_ids, teacher_logits, row_weight=None, *, temper
                                               out, status)
 
 
+class _DistillGradient(torch.autograd.Function):
+    """The loss's gradient; its own derivatives are not built, and asking for them is an error."""
+
+    @staticmethod
+    def forward(ctx, logits, grad, teacher_ids, teacher_logits, stats, temperature):
+        return distill_backward(logits, teacher_ids, teacher_logits, stats, grad, temperature=temperature)
+
+    @staticmethod
+    def backward(ctx, grad):
+        raise RuntimeError("distill_loss can be differentiated only once")
+
+
 class _DistillLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, teacher_ids, teacher_logits, temperature, teacher_lse):
@@ -96,11 +108,10 @@ class _DistillLoss(torch.autograd.Function):
         return loss
 
     @staticmethod
-    @torch.autograd.function.once_differentiable  # the gradient's own derivatives are not built
     def backward(ctx, grad):
         logits, ids, teacher, stats = ctx.saved_tensors
-        return (distill_backward(logits, ids, teacher, stats, grad.float().contiguous(),
-                                 temperature=ctx.temperature), None, None, None, None)
+        return (_DistillGradient.apply(logits, grad.float().contiguous(), ids, teacher, stats, ctx.temperature), None,
+                None, None, None)
 
 
 def distill_loss(logits, teacher_ids, teacher_logits, *, temperature=1.0, teacher_lse=None):
