@@ -4,6 +4,7 @@
 // host time, most of it the launch; the same checks in Python over ctypes cost 15.
 #include <Python.h>
 #include <ATen/ATen.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -34,6 +35,19 @@ template <typename... A>
 const at::Tensor& tensor(PyObject* o, const char* name) {
   if (!THPVariable_Check(o)) refuse("%s must be a tensor", name);
   return THPVariable_Unpack(o);
+}
+
+// A caller's tensor that the call writes to. Autograd's rules for operations in place hold: no
+// leaf that takes a gradient (nor a view of one) while gradients are recorded, and a new
+// version, so that a backward that saved the old values raises.
+const at::Tensor& target(PyObject* o, const char* name) {
+  const at::Tensor& t = tensor(o, name);
+  if (c10::GradMode::is_enabled() && t.requires_grad() && (t.is_leaf() || (t.is_view() && t._base().is_leaf())))
+    refuse("%s is a leaf (or a view of one) that requires a gradient: it cannot be written in place", name);
+  return t;
+}
+void written(const at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
 }
 
 int dtype_code(at::ScalarType t) {
@@ -170,13 +184,14 @@ PyObject* process_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
       mask = static_cast<const uint32_t*>(m.data_ptr()), mask_stride = m.stride(0);
     }
     const at::ScalarType type = a[9] == Py_None ? z.t.scalar_type() : type_of(a[9]);
-    const Matrix y(a[8] == Py_None ? empty({B, V}, type, dev) : tensor(a[8], "out"), "out");
+    const Matrix y(a[8] == Py_None ? empty({B, V}, type, dev) : target(a[8], "out"), "out");
     y.wants(B, V, dev, "out");
     if (a[9] != Py_None && y.t.scalar_type() != type) refuse("out has another type than dtype");
     check(lib.logits_process(dev, z.ptr(), z.dtype, z.stride, B, V, p.ids, p.offsets, p.n, o.ids, o.offsets, o.n, rep,
                              freq, pres, b.ids, b.offsets, values, b.n, mask, mask_stride, y.ptr(), y.dtype, y.stride,
                              status_word(a[10], dev), stream(dev)),
           "emb_logits_process");
+    written(y.t);
     return THPVariable_Wrap(y.t);
   });
 }
@@ -207,7 +222,7 @@ struct Rows {
     const int64_t piece = 16 / (int64_t)z.t.element_size();
     const bool alike = N > 1 && z.stride > V && reinterpret_cast<uintptr_t>(z.ptr()) % 16 == 0;
     const int64_t stride = V + (alike ? (z.stride - V) % piece : 0);
-    const Matrix g(out == Py_None ? at::empty_strided({N, V}, {stride, 1}, z.t.options()) : tensor(out, "out"), "out");
+    const Matrix g(out == Py_None ? at::empty_strided({N, V}, {stride, 1}, z.t.options()) : target(out, "out"), "out");
     g.wants(N, V, z.device, "out");
     if (g.dtype != z.dtype) refuse("out must have the type of logits");
     return g;
@@ -238,6 +253,7 @@ PyObject* distill_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                r.K, r.of_rows(a[3], 4, "stats"), r.of_rows(a[4], 1, "row_weight"), real(a[5]), g.ptr(),
                                g.stride, status_word(a[7], dev), stream(dev)),
           "emb_distill_backward");
+    written(g.t);
     return THPVariable_Wrap(g.t);
   });
 }
@@ -253,6 +269,7 @@ PyObject* distill_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
                            r.of_rows(a[5], 1, "teacher_lse"), r.of_rows(a[3], 1, "row_weight"), real(a[4]),
                            static_cast<float*>(loss.data_ptr()), g.ptr(), g.stride, status_word(a[7], dev), stream(dev)),
           "emb_distill_step");
+    written(g.t);
     return pair(std::move(loss), g.t);
   });
 }
@@ -289,7 +306,7 @@ PyObject* micro_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
       codes = empty({x.rows, row_bytes(x.cols)}, at::kByte, dev);
       scales = empty({(x.rows + 127) / 128, scale_tiles(x.cols, format), 32, 4, 4}, at::kByte, dev);
     } else {
-      codes = tensor(a[3], "out"), scales = tensor(a[4], "out");
+      codes = target(a[3], "out"), scales = target(a[4], "out");
       vector<uint8_t>(a[3], dev, at::kByte, x.rows * row_bytes(x.cols), "codes of out");
       vector<uint8_t>(a[4], dev, at::kByte, (x.rows + 127) / 128 * scale_tiles(x.cols, format) * 512, "scales of out");
     }
@@ -297,6 +314,8 @@ PyObject* micro_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
                              real(a[2]), static_cast<uint8_t*>(codes.data_ptr()),
                              static_cast<uint8_t*>(scales.data_ptr()), stream(dev)),
           "emb_micro_quantize");
+    written(codes);
+    written(scales);
     return pair(std::move(codes), std::move(scales));
   });
 }
@@ -307,11 +326,12 @@ PyObject* micro_lookup(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Micro m(a, "table");
     const int64_t count = a[6] == Py_None ? m.rows : tensor(a[6], "ids").numel();
     const int64_t* ids = vector<int64_t>(a[6], m.device, at::kLong, count, "ids");
-    const Matrix y(a[8] == Py_None ? empty({count, m.cols}, type_of(a[7]), m.device) : tensor(a[8], "out"), "out");
+    const Matrix y(a[8] == Py_None ? empty({count, m.cols}, type_of(a[7]), m.device) : target(a[8], "out"), "out");
     y.wants(count, m.cols, m.device, "out");
     check(lib.micro_lookup(m.device, m.codes, m.scales, m.rows, size32(m.cols, "table"), m.format, m.g, ids, count, y.ptr(),
                            y.dtype, y.stride, status_word(a[9], m.device), stream(m.device)),
           "emb_micro_lookup");
+    written(y.t);
     return THPVariable_Wrap(y.t);
   });
 }
@@ -323,11 +343,12 @@ PyObject* micro_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (w.format != x.format || w.cols != x.cols || w.device != x.device)
       refuse("x and w must have the same format, columns and device");
     const int32_t M = size32(x.rows, "x"), N = size32(w.rows, "w");
-    const Matrix y(a[13] == Py_None ? empty({M, N}, type_of(a[12]), x.device) : tensor(a[13], "out"), "out");
+    const Matrix y(a[13] == Py_None ? empty({M, N}, type_of(a[12]), x.device) : target(a[13], "out"), "out");
     y.wants(M, N, x.device, "out");
     check(lib.micro_matmul(x.device, x.codes, x.scales, x.g, M, w.codes, w.scales, w.g, N, size32(x.cols, "x"), x.format,
                            y.ptr(), y.dtype, y.stride, status_word(a[14], x.device), stream(x.device)),
           "emb_micro_matmul");
+    written(y.t);
     return THPVariable_Wrap(y.t);
   });
 }

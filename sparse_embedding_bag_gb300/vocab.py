@@ -14,6 +14,9 @@ kernels called on the current stream of the tensors' device, by the compiled ent
 the C header. Malformed arguments raise ValueError, a status of the library EmbError. ``status`` is
 an int32 tensor of one element that collects device error bits (1: an id out of range, 2:
 malformed offsets, 4: a bounded wait ran out); the caller clears it.
+
+Of these only ``distill_loss`` takes part in autograd: the other calls take tensors that require
+gradients as values, and what they return has no history. An ``out`` counts as changed in place.
 """
 from __future__ import annotations
 
