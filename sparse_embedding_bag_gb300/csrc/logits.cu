@@ -168,6 +168,77 @@ struct Lists {
   int64_t ps, pe, os, oe, bs, be;
 };
 
+// Groups of eight start `head` tokens into a piece, so that stores are 16-byte aligned, and
+// loads too where input and output allow it together.
+template <typename in_t, typename out_t>
+__device__ __forceinline__ int32_t head_of(const in_t* z, const out_t* y, int32_t len, bool* wide_loads) {
+  constexpr uint32_t in_n = 16 / sizeof(in_t), out_n = 16 / sizeof(out_t), both_n = in_n < out_n ? in_n : out_n;
+  const uint32_t in_at = (uint32_t)(reinterpret_cast<uintptr_t>(z) / sizeof(in_t)) % in_n;
+  const uint32_t out_at = (uint32_t)(reinterpret_cast<uintptr_t>(y) / sizeof(out_t)) % out_n;
+  *wide_loads = in_at % both_n == out_at % both_n;
+  return min(len, (int32_t)(*wide_loads && in_n > out_n ? -in_at % in_n : -out_at % out_n));
+}
+
+// The biased tokens of a piece where the list names one twice. A warp takes 512 of the piece's
+// tokens at a time, a lane 16 of them, and goes over the list: every token's biases add in
+// list order, and the work is (tokens of the piece / 4096) times the list's length.
+template <typename in_t, typename out_t, int kBits>
+__device__ __forceinline__ void add_biases(const LogitsArgs& a, int32_t b, int32_t v0, int32_t len, const Lists& l,
+                                           const Penalty& penalty, const uint32_t* smem) {
+  using C = Counts<kBits>;
+  const in_t* z = static_cast<const in_t*>(a.z) + b * a.z_stride + v0;
+  out_t* y = static_cast<out_t*>(a.y) + b * a.y_stride + v0;
+  const uint32_t* mask = a.mask ? a.mask + b * a.mask_stride : nullptr;
+  bool wide_loads;
+  const C counts{smem_u32(smem), (uint32_t)(-head_of(z, y, len, &wide_loads) & 7)};
+  constexpr int kOwn = 16, kAhead = 4;  // a lane's tokens, its entries in flight
+  constexpr int32_t kWindow = kOwn * 32;
+  const int32_t lane = threadIdx.x & 31;
+  for (int32_t at = (threadIdx.x >> 5) * kWindow; at < len; at += kLogitThreads / 32 * kWindow) {
+    float sum[kOwn];
+    uint32_t mine = 0;
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) {
+      const int32_t off = at + k * 32 + lane;
+      const uint32_t c = off < len ? counts.get(off) : 0;
+      sum[k] = 0.f;
+      if (c & C::kBias) sum[k] = penalty(Elem<in_t>::get(z[off]), c & ~C::kBias, c & C::kTimes), mine |= 1u << k;
+    }
+    if (!__any_sync(0xffffffffu, mine)) continue;
+    const int64_t first = (int64_t)v0 + at, count = min(kWindow, len - at);
+    for (int64_t j0 = l.bs; j0 < l.be; j0 += 32 * kAhead) {
+      int64_t token[kAhead];
+      float bias[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int64_t j = j0 + i * 32 + lane;
+        token[i] = j < l.be ? a.b_ids[j] : -1;
+        bias[i] = j < l.be ? a.b_val[j] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int64_t o = token[i] - first;
+        for (uint32_t here = __ballot_sync(0xffffffffu, o >= 0 && o < count); here; here &= here - 1) {
+          const int from = __ffs(here) - 1;
+          const int32_t off = __shfl_sync(0xffffffffu, (int32_t)o, from);
+          const float x = __shfl_sync(0xffffffffu, bias[i], from);
+          if (off % 32 != lane) continue;
+#pragma unroll
+          for (int k = 0; k < kOwn; ++k)
+            if (off / 32 == k) sum[k] += x;
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k)
+      if (mine >> k & 1u) {
+        const int32_t off = at + k * 32 + lane;
+        const uint32_t v = v0 + off;
+        y[off] = Elem<out_t>::put(!mask || (mask[v >> 5] >> (v & 31) & 1u) ? sum[k] : -INFINITY);
+      }
+  }
+}
+
 // Tokens [v0, v0 + len) of request b. kBits 0: there are no lists.
 template <typename in_t, typename out_t, int kBits>
 __device__ __forceinline__ void process(const LogitsArgs& a, int32_t b, int32_t v0, int32_t len, const Lists& l,
@@ -175,13 +246,8 @@ __device__ __forceinline__ void process(const LogitsArgs& a, int32_t b, int32_t 
   using C = Counts<kBits ? kBits : 32>;
   const in_t* z = static_cast<const in_t*>(a.z) + b * a.z_stride + v0;
   out_t* y = static_cast<out_t*>(a.y) + b * a.y_stride + v0;
-  // Groups of eight start `head` tokens into the piece, so that stores are 16-byte
-  // aligned, and loads too where input and output allow it together.
-  constexpr uint32_t in_n = 16 / sizeof(in_t), out_n = 16 / sizeof(out_t), both_n = in_n < out_n ? in_n : out_n;
-  const uint32_t in_at = (uint32_t)(reinterpret_cast<uintptr_t>(z) / sizeof(in_t)) % in_n;
-  const uint32_t out_at = (uint32_t)(reinterpret_cast<uintptr_t>(y) / sizeof(out_t)) % out_n;
-  const bool wide_loads = in_at % both_n == out_at % both_n;
-  const int32_t head = min(len, (int32_t)(wide_loads && in_n > out_n ? -in_at % in_n : -out_at % out_n));
+  bool wide_loads;
+  const int32_t head = head_of(z, y, len, &wide_loads);
   const int32_t groups = (len - head) / kGroup;
   const C counts{smem_u32(smem), (uint32_t)(-head & 7)};
   const uint32_t* mask = a.mask ? a.mask + b * a.mask_stride : nullptr;
@@ -276,21 +342,14 @@ __device__ __forceinline__ void process(const LogitsArgs& a, int32_t b, int32_t 
     const uint32_t c = kBits ? counts.get(at) : 0;
     if (!(c & C::kBias)) y[at] = Elem<out_t>::put(allowed(v0 + at) ? penalised(Elem<in_t>::get(z[at]), c) : -INFINITY);
   }
-  // Each biased token by the thread of its first entry; its biases in list order.
-  for (int64_t j = l.bs + threadIdx.x; kBits && j < l.be; j += kLogitThreads) {
+  if (!kBits || *repeated) return;
+  // each biased token by the thread of its entry
+  for (int64_t j = l.bs + threadIdx.x; j < l.be; j += kLogitThreads) {
     const bool first = j == l.bs + threadIdx.x;
     const int64_t v = first ? own_id : a.b_ids[j];
     if (v < v0 || v >= v0 + len) continue;
-    bool mine = true;
-    if (*repeated)
-      for (int64_t i = l.bs; i < j && mine; ++i) mine = a.b_ids[i] != v;
-    if (!mine) continue;
-    float x = penalised(first ? own_z : Elem<in_t>::get(z[v - v0]), counts.get((uint32_t)(v - v0))) +
-              (first ? own_bias : a.b_val[j]);
-    if (*repeated)
-      for (int64_t i = j + 1; i < l.be; ++i)
-        if (a.b_ids[i] == v) x += a.b_val[i];
-    y[v - v0] = Elem<out_t>::put(allowed((uint32_t)v) ? x : -INFINITY);
+    const float x = penalised(first ? own_z : Elem<in_t>::get(z[v - v0]), counts.get((uint32_t)(v - v0)));
+    y[v - v0] = Elem<out_t>::put(allowed((uint32_t)v) ? x + (first ? own_bias : a.b_val[j]) : -INFINITY);
   }
 }
 
@@ -299,6 +358,7 @@ template <typename in_t, typename out_t>
 __device__ __noinline__ void process_long(const LogitsArgs& a, int32_t b, int32_t v0, int32_t len, const Lists& l,
                                           const Penalty& penalty, uint32_t* smem, int* repeated) {
   process<in_t, out_t, 32>(a, b, v0, len, l, penalty, smem, repeated);
+  if (*repeated) add_biases<in_t, out_t, 32>(a, b, v0, len, l, penalty, smem);
 }
 
 template <typename in_t, typename out_t, bool kLists>
@@ -321,6 +381,7 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitBlocks) k_logits(LogitsAr
   if (a.b_ids) list_of(a.b_off, a.b_n, b, a.status, &l.bs, &l.be);
   if (l.oe - l.os <= (int64_t)Counts<16>::kTimes) {
     process<in_t, out_t, 16>(a, b, v0, len, l, penalty, smem, &repeated);
+    if (repeated) add_biases<in_t, out_t, 16>(a, b, v0, len, l, penalty, smem);
     return;
   }
   const int32_t half = a.slice / 2;  // the room of a slice's 16-bit entries
