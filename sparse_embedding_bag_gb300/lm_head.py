@@ -28,12 +28,15 @@ def csr(lists, device):
 
 
 def serve(table, layer, prompts, steps, *, format="nv", mask=None, repetition=1.2, frequency=0.1, bias=None):
-    """Greedy continuations of ``prompts`` (lists of token ids): a list of ``steps`` ids each.
+    """Greedy continuations of ``prompts`` (lists of token ids, none empty): a list of ``steps`` ids each.
 
     table [V, D] bf16, layer [D, D] bf16; mask int32 [B, ceil(V / 32)]; bias (ids, offsets, values).
     """
     device, B = table.device, len(prompts)
-    scale = float(table.abs().max()) / (6 * 448) if format == "nv" else 1.0
+    # tensor scales that spread the largest magnitude over the block scales: the table's, and 1 for
+    # hidden states, which tanh bounds (so that no step waits for its own); a table of zeros takes any
+    scale = float(table.abs().max()) / (6 * 448) or 1.0 if format == "nv" else 1.0
+    x_scale = 1 / (6 * 448) if format == "nv" else 1.0
     packed = vocab.micro_quantize(table, format, scale)
     prompt = csr(prompts, device)
     rep = torch.full((B,), repetition, device=device)
@@ -43,7 +46,6 @@ def serve(table, layer, prompts, steps, *, format="nv", mask=None, repetition=1.
     status = torch.zeros(1, dtype=torch.int32, device=device)
     for step in range(steps):
         hidden = torch.tanh(vocab.micro_lookup(packed, last, dtype=table.dtype, status=status) @ layer)
-        x_scale = float(hidden.abs().max()) / (6 * 448) if format == "nv" else 1.0
         logits = vocab.micro_matmul(vocab.micro_quantize(hidden, format, x_scale), packed, dtype=torch.float32,
                                     status=status)
         output = (said.reshape(-1), torch.arange(0, B * step + 1, step, device=device)) if step else None
