@@ -364,7 +364,7 @@ emb_status emb_shard_status(emb_shard* shard);
  * device_status (device uint32, may be NULL) collects device error bits: they are
  * added to it (the caller clears it) - 1 = an id outside its range (the entry is
  * left out), 2 = malformed CSR offsets (the list is taken as empty), 4 = a bounded
- * wait ran out (the output is not valid). */
+ * wait ran out (what was not finished of the output is NaN). */
 
 /* Logits before a token is chosen. B requests (<= 65535), V tokens (<= 2^20). For
  * token v of request b, with z its logit and c the times v occurs in the request's

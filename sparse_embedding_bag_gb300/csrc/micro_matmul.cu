@@ -93,6 +93,14 @@ __device__ __forceinline__ void store_columns(const MatmulArgs& a, uint32_t tmem
   }
 }
 
+// NaN in place of a tile that was given up.
+template <typename T>
+__device__ __forceinline__ void store_nan(const MatmulArgs& a, int32_t n, int32_t m0, int32_t cols) {
+  if (n >= a.N) return;
+  for (int32_t m = m0; m < min(a.M, m0 + cols); ++m)
+    static_cast<T*>(a.out)[(int64_t)m * a.out_stride + n] = Elem<T>::put(NAN);
+}
+
 template <typename T, int kFormat, int kTok, bool kPair>
 __global__ void __launch_bounds__(kMatmulThreads, 1)
     k_micro_matmul(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap wsmap,
@@ -162,10 +170,11 @@ __global__ void __launch_bounds__(kMatmulThreads, 1)
         if (++s == S::kStages) s = 0, ++round;
       }
     }
-    // Copies of an abandoned tile may be in flight: no copy takes a millisecond.
-    if (!ok)
-      for (const uint64_t t0 = global_ns(); global_ns() - t0 < 1000000;) {
-      }
+    // A CTA of a pair stays until its last stages are free: CTA 0's MMAs bring the news.
+    for (uint32_t i = 0; kPair && i < S::kStages && ok; ++i) {
+      if (round) ok = mbar_wait<kPair>(smem_u32(&ctl.empty[s]), (round - 1) & 1, abort);
+      if (++s == S::kStages) s = 0, ++round;
+    }
   } else if (warp == 5 && rank == 0) {
     // A: table codes, B: token codes, both E2M1, fp32 sums (bits 7, 10); tokens / 8 (17); E8M0 scales (23); rows / 128 (27)
     constexpr uint32_t idesc0 = 1u << 7 | 1u << 10 | (kFormat == kMicroMX ? 1u << 23 : 0u) | S::kCtas << 27;
@@ -182,20 +191,18 @@ __global__ void __launch_bounds__(kMatmulThreads, 1)
     bool ok = true;
     for (int64_t t = first; t < tiles && ok; t += step, ++j) {
       constexpr uint32_t lag = S::kShared ? 1 : 2;  // the tile whose columns this one takes over
-      if (j >= lag && !mbar_wait<kPair>(smem_u32(&ctl.acc_empty[(j - lag) & 1]), ((j - lag) >> 1) & 1, abort)) break;
+      ok = j < lag || mbar_wait<kPair>(smem_u32(&ctl.acc_empty[(j - lag) & 1]), ((j - lag) >> 1) & 1, abort);
+      if (!__all_sync(0xffffffffu, ok)) break;
       const uint32_t d = tmem + ((j & 1) ? S::kAcc1 : 0);
       const int32_t left = a.M - (int32_t)(t % x_tiles) * kTok;
       const uint32_t toks = (uint32_t)(min(kTok, left) + 16 * (int32_t)S::kCtas - 1) / (16 * S::kCtas) * (16 * S::kCtas);
       const uint32_t idesc = idesc0 | toks / 8 << 17;
       for (int32_t k = 0; k < k_stages; ++k) {
-        if (!mbar_wait<kPair>(full0 + s * 8, parity, abort)) {
-          ok = false;
-          break;
-        }
+        ok = mbar_wait<kPair>(full0 + s * 8, parity, abort);
         tc_fence_after();
         const uint64_t a_desc = a_desc0 + s * kBlock, b_desc = a_desc + (S::kA >> 4), sf_desc = sf_desc0 + s * kBlock;
         const int32_t used = sf_tiles - k * (int32_t)S::kTiles, steps = (a.K - k * kDepth + kStep - 1) / kStep;
-        if (leader) {
+        if (leader && ok) {
 #pragma unroll
           for (int i = 0; i < (int)S::kTiles; ++i) {
             if (i >= used) break;
@@ -217,7 +224,8 @@ __global__ void __launch_bounds__(kMatmulThreads, 1)
           tc_commit<kPair>(empty0 + s * 8);
           if (k + 1 == k_stages) tc_commit<kPair>(smem_u32(&ctl.acc_full[j & 1]));
         }
-        __syncwarp();
+        ok = __all_sync(0xffffffffu, ok);  // all lanes leave if one has given up
+        if (!ok) break;
         if (++s == S::kStages) s = 0, parity ^= 1;
       }
     }
@@ -232,13 +240,17 @@ __global__ void __launch_bounds__(kMatmulThreads, 1)
       else
         mbar_arrive(smem_u32(&ctl.acc_empty[j & 1]));
     };
+    bool ok = true;
     for (int64_t t = first; t < tiles; t += step, ++j) {
       const int32_t wt = (int32_t)(t / x_tiles), xt = (int32_t)(t - (int64_t)wt * x_tiles);
-      const bool ok = mbar_wait<kPair>(smem_u32(&ctl.acc_full[j & 1]), (j >> 1) & 1, abort);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      const int32_t n = wt * kRows * (int32_t)S::kCtas + (int32_t)(rank * kRows + warp * 32 + lane);
+      ok = ok && __all_sync(0xffffffffu, mbar_wait<kPair>(smem_u32(&ctl.acc_full[j & 1]), (j >> 1) & 1, abort));
+      if (!ok) {  // the tiles that will not come
+        store_nan<T>(a, n, xt * kTok, kTok);
+        continue;
+      }
       tc_fence_after();
       const uint32_t d = tmem + ((j & 1) ? S::kAcc1 : 0) + (warp * 32 << 16);
-      const int32_t n = wt * kRows * (int32_t)S::kCtas + (int32_t)(rank * kRows + warp * 32 + lane);
       const uint32_t shared0 = (j & 1) ? 0 : kTok - S::kShared;  // the shared columns come first
       store_columns<T>(a, d, n, xt * kTok, shared0, shared0 + S::kShared);
       if (S::kShared) emptied();
@@ -249,11 +261,9 @@ __global__ void __launch_bounds__(kMatmulThreads, 1)
   __syncwarp();
   // Nothing may be in flight when the tensor memory goes back, nor when a CTA that holds
   // the pair's barriers or operands ends.
-  if (warp == 5 && lane == 0 && rank == 0) {
-    const uint64_t t0 = global_ns();
-    while (!mbar_try(smem_u32(&ctl.done), 0) && global_ns() - t0 < kWaitNs) {
+  if (warp == 5 && lane == 0 && rank == 0)
+    for (Patience p; !mbar_try(smem_u32(&ctl.done), 0) && !p.over(kDrainNs);) {
     }
-  }
   __syncwarp();
   tc_fence_before();
   if (kPair)
@@ -261,7 +271,12 @@ __global__ void __launch_bounds__(kMatmulThreads, 1)
   else
     __syncthreads();
   tc_fence_after();
-  if (threadIdx.x == 0 && *abort) report(a.status, kErrTimeout);
+  if (*abort) {
+    // Copies of abandoned stages may be on their way to this CTA: none takes a millisecond.
+    for (Patience p; !p.over(1000000);) {
+    }
+    if (threadIdx.x == 0) report(a.status, kErrTimeout);
+  }
   if (warp == 5) tmem_dealloc<kPair>(tmem, kTmemCols);
 }
 

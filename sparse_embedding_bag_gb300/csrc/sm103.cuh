@@ -57,7 +57,24 @@ struct F2 {
 
 // ---- mbarriers
 
-constexpr uint64_t kWaitNs = 2000000000ull;  // a wait gives up after two seconds
+#ifndef EMB_WAIT_NS  // a test builds the library with waits that run out at once
+#define EMB_WAIT_NS 2000000000ull
+#endif
+constexpr uint64_t kWaitNs = EMB_WAIT_NS;     // a wait gives up after two seconds
+constexpr uint64_t kDrainNs = 2000000000ull;  // and one for work that is known to be under way
+
+// The time that a wait has spent. What passes between two looks at the clock counts as ten
+// milliseconds at most: a process that was suspended or lost its time slice for seconds has
+// not waited for them.
+struct Patience {
+  uint64_t last = global_ns(), spent = 0;
+  __device__ __forceinline__ bool over(uint64_t limit) {
+    const uint64_t now = global_ns(), passed = now - last;
+    spent += passed < 10000000 ? passed : 10000000;
+    last = now;
+    return spent > limit;
+  }
+};
 
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
@@ -93,20 +110,9 @@ __device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity) 
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// Waits for the phase with that parity to complete; false after two seconds, or as
-// soon as another role of the block has given up (`*abort` set).
-template <bool kCluster = false>
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-  if (kCluster ? mbar_try_cluster(bar, parity) : mbar_try(bar, parity)) return true;
-  const uint64_t t0 = global_ns();
-  for (;;) {
-    for (int i = 0; i < 64; ++i)
-      if (kCluster ? mbar_try_cluster(bar, parity) : mbar_try(bar, parity)) return true;
-    if (*abort || global_ns() - t0 > kWaitNs) {
-      *abort = 1;
-      return false;
-    }
-  }
+template <bool kCluster>
+__device__ __forceinline__ bool mbar_tries(uint32_t bar, uint32_t parity) {
+  return kCluster ? mbar_try_cluster(bar, parity) : mbar_try(bar, parity);
 }
 
 // ---- clusters
@@ -133,6 +139,33 @@ __device__ __forceinline__ uint32_t cluster_map(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void cluster_store(uint32_t addr, float4 v) {
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
                : "memory");
+}
+
+// ---- bounded waits. `*abort` is a flag in shared memory, set by the first wait of a block (kPair:
+// of a pair of CTAs, where both have it at the same address) that gives up; the others then
+// do so too.
+
+template <bool kPair>
+__device__ __forceinline__ void give_up(volatile int* abort) {
+  *abort = 1;
+  if (kPair)
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_map(smem_u32(const_cast<int*>(abort)), cluster_rank() ^ 1)),
+                 "r"(1)
+                 : "memory");
+}
+// Waits for the phase with that parity to complete; false if it does not. Lanes that wait
+// together may differ in the answer.
+template <bool kPair>
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  if (mbar_tries<kPair>(bar, parity)) return true;
+  for (Patience p;;) {
+    for (int i = 0; i < 8; ++i)
+      if (mbar_tries<kPair>(bar, parity)) return true;
+    if (*abort || p.over(kWaitNs)) {
+      give_up<kPair>(abort);
+      return false;
+    }
+  }
 }
 
 // ---- copies

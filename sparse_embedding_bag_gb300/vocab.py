@@ -13,7 +13,8 @@ kernels called on the current stream of the tensors' device, by the compiled ent
 (one call's host work counts beside a kernel of a few microseconds). Formulas and layouts are in
 the C header. Malformed arguments raise ValueError, a status of the library EmbError. ``status`` is
 an int32 tensor of one element that collects device error bits (1: an id out of range, 2:
-malformed offsets, 4: a bounded wait ran out); the caller clears it.
+malformed offsets, 4: a bounded wait of a product ran out, and what was not finished is NaN); the
+caller clears it.
 
 Of these only ``distill_loss`` takes part in autograd: the other calls take tensors that require
 gradients as values, and what they return has no history. An ``out`` counts as changed in place.
