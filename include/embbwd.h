@@ -374,8 +374,10 @@ emb_status emb_shard_status(emb_shard* shard);
  *   z <- z + the biases of v, in the order of the list
  *   bit v % 32 of mask[b, v / 32] clear:  z <- -infinity
  * in fp32 (the division as a product with the reciprocal), rounded once to out_dtype.
- * prompt/output/bias lists are CSR: ids int64[n], n < 2^31, offsets int64[B+1] with values in 0..n (both NULL and n = 0: no list; a bias list
- * has fp32 bias_values). repetition, frequency, presence: fp32[B], NULL = 1, 0, 0.
+ * prompt/output/bias lists are CSR: ids int64[n], n < 2^31, offsets int64[B+1] with values in
+ * 0..n (both NULL and n = 0: no list; a bias list has fp32 bias_values). A request has fewer
+ * than 2^30 output ids (a longer list counts as malformed offsets).
+ * repetition, frequency, presence: fp32[B], NULL = 1, 0, 0.
  * mask: uint32 [B, mask_stride >= ceil(V / 32)] or NULL. `out` may be `logits` itself
  * (same type and stride), and must not overlap it otherwise. */
 emb_status emb_logits_process(int device, const void* logits, emb_dtype logits_dtype,

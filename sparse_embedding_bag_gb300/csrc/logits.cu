@@ -47,12 +47,13 @@ struct LogitsArgs {
 };
 
 
-// [start, end) of request b's list, empty (and reported) if the offsets are malformed.
+// [start, end) of request b's list, empty (and reported) if the offsets are malformed or the
+// list is longer than `most`.
 __device__ __forceinline__ void list_of(const int64_t* off, int64_t n, int32_t b, uint32_t* status, int64_t* start,
-                                        int64_t* end) {
+                                        int64_t* end, int64_t most = INT32_MAX) {
   *start = off[b];
   *end = off[b + 1];
-  if (*start < 0 || *end < *start || *end > n) {
+  if (*start < 0 || *end < *start || *end > n || *end - *start > most) {
     report(status, kErrOffsets);
     *start = *end = 0;
   }
@@ -377,7 +378,7 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitBlocks) k_logits(LogitsAr
     return;
   }
   if (a.p_ids) list_of(a.p_off, a.p_n, b, a.status, &l.ps, &l.pe);
-  if (a.o_ids) list_of(a.o_off, a.o_n, b, a.status, &l.os, &l.oe);
+  if (a.o_ids) list_of(a.o_off, a.o_n, b, a.status, &l.os, &l.oe, Counts<32>::kTimes);  // more are not counted
   if (a.b_ids) list_of(a.b_off, a.b_n, b, a.status, &l.bs, &l.be);
   if (l.oe - l.os <= (int64_t)Counts<16>::kTimes) {
     process<in_t, out_t, 16>(a, b, v0, len, l, penalty, smem, &repeated);

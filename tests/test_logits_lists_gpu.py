@@ -105,3 +105,17 @@ def test_a_repeated_bias_does_not_make_a_long_list_quadratic(V):
     plain, repeated = ms(ids), ms(twice)
     print(f"distinct {plain * 1e3:.0f} us, one repeated {repeated * 1e3:.0f} us")
     assert repeated < 10 * plain
+
+
+def test_an_output_list_too_long_to_count(V):
+    # 2^30 times one token would run into the flags beside its count
+    n = (1 << 30) + 5
+    ids, z = torch.full((n + 3,), 2, dtype=torch.int64, device="cuda"), torch.randn(2, 100, device="cuda")
+    ids[-3:] = 7
+    ones, status = torch.ones(2, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = V.process_logits(z, output=(ids, torch.tensor([0, n, n + 3], device="cuda")), frequency=ones, presence=ones,
+                           status=status)
+    want = z.clone()
+    want[1, 7] = want[1, 7] - 3 - 1
+    assert status.item() == 2
+    torch.testing.assert_close(got, want, rtol=1e-6, atol=1e-6)
