@@ -1,5 +1,6 @@
 """Builds libembbwd.so in-tree: every csrc/*.cu compiled for sm_103a in parallel, then linked;
-and _vocab.so, the Python entry of the vocabulary operators (csrc/vocab_torch.cpp), beside it.
+and, where there is a PyTorch with CUDA, _vocab.so, the Python entry of the vocabulary operators
+(csrc/vocab_torch.cpp), beside it.
 
     python -m sparse_embedding_bag_gb300.build [--force] [--ptxas-v]
 """
@@ -7,6 +8,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -30,13 +32,17 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def build_entry() -> str:
+def build_entry() -> None:
     """_vocab.so: host code against this machine's PyTorch headers (no link to libembbwd: it is
-    given the functions' addresses when it is loaded)."""
+    given the functions' addresses when it is loaded). The library itself does without PyTorch."""
     import sysconfig
 
+    if not has_torch():
+        return
     import torch
     from torch.utils import cpp_extension
+    if torch.version.cuda is None:
+        return
     include = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"],
                os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
@@ -49,7 +55,10 @@ def build_entry() -> str:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {ENTRY_SRC}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, ENTRY)
-    return ENTRY
+
+
+def has_torch() -> bool:
+    return importlib.util.find_spec("torch") is not None
 
 
 def _newest(paths):
@@ -60,7 +69,8 @@ def build(force: bool = False, ptxas_verbose: bool = False, jobs: int | None = N
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     deps = srcs + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
     newest = _newest(deps + [ENTRY_SRC, __file__])
-    if not force and all(os.path.exists(p) and os.path.getmtime(p) >= newest for p in (LIB, ENTRY)):
+    made = (LIB, ENTRY) if has_torch() else (LIB,)
+    if not force and all(os.path.exists(p) and os.path.getmtime(p) >= newest for p in made):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
