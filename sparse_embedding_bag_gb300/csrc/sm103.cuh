@@ -43,11 +43,6 @@ struct F2 {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(u), "l"(o.u));
     return r;
   }
-  __device__ __forceinline__ F2 fma(F2 b, F2 c) const {  // this * b + c
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.u) : "l"(u), "l"(b.u), "l"(c.u));
-    return r;
-  }
   __device__ __forceinline__ F2 operator*(F2 o) const {
     F2 r;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(u), "l"(o.u));
