@@ -412,7 +412,8 @@ emb_status emb_logits_process(int device, const void* logits, emb_dtype logits_d
  *   emb_distill_backward  dlogits (logits_dtype) = row_weight[n] * dloss/dz from the
  *                         forward's stats; row_weight fp32[N] or NULL = 1
  *   emb_distill_step      loss and dlogits in one call, for a row_weight known
- *                         beforehand; z is read from HBM once
+ *                         beforehand; z is read twice, the second time from L2 while
+ *                         the rows under way fit it (16-bit rows of 128256 do)
  * dlogits may be logits itself (same stride) and must not overlap it otherwise. */
 emb_status emb_distill_forward(int device, const void* logits, emb_dtype logits_dtype,
                                int64_t logits_stride, int32_t N, int32_t V,

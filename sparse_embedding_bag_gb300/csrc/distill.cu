@@ -11,9 +11,9 @@
 // u is summed over the tokens off the list, never as 1 - (mass on it): it would
 // cancel for a student that agrees with its teacher. The sum is relative to a
 // reference near the largest logit off the list: relative to the row's largest, which is
-// usually a listed one, it underflows once the listed tokens lead by 87 tau. Entries with id -1 are
-// padding; a row without entries, or whose teacher has no mass (L = -infinity), has
-// loss 0 and gradient 0. With no finite logit off the list u is 0: an r that rounding
+// usually a listed one, it underflows once the listed tokens lead by 87 tau. Entries with
+// id -1 are padding; a row without entries, or whose teacher has no mass (L = -infinity),
+// has loss 0 and gradient 0. With no finite logit off the list u is 0: an r that rounding
 // explains counts as 0, a larger one makes the loss infinite; either way the gradient
 // off the list is 0.
 //
@@ -24,11 +24,15 @@
 // Forward and step: a cluster of CTAs takes a row, a part of it each. It streams its part
 // from HBM with a running reference (sums are rescaled when a value exceeds it by far, which
 // is rare after the first), the cluster exchanges largest logits and sums through
-// distributed shared memory in one round, and the step streams the part once more: it is
-// still in L2 (all rows under way are a third of it), so HBM sees one read and one write.
+// distributed shared memory in one round, and the step streams the part once more. Rows of
+// 128256 16-bit logits are still in L2 then (49 MB under way of its 129): HBM reads 269 MB
+// for 263 MB of rows. fp32 rows of that length mostly are not (97 MB under way, and their
+// gradients: 972 MB for 525), nor are rows of 2^20, whose parts are longer (bf16 1075 MB for
+// 537, fp32 2150 for 1074). 4096 x 128256 bf16 take 388 us (5.3 TB/s of one read and one
+// write), fp32 905 (4.6); 256 x 2^20 bf16 249 (4.3), fp32 515 (4.2).
 // Backward (its sums are known): blocks over pieces of the rows, one read and one write.
 // Holding the rows in shared memory instead (bulk copies, three CTAs of 64 KB an SM) took
-// 474 us a step at 4096 x 128256 bf16, against 395: a CTA does nothing else while its
+// 474 us a step at 4096 x 128256 bf16, against 388: a CTA does nothing else while its
 // slice arrives, and reads it three times.
 #include <cmath>
 
@@ -562,9 +566,10 @@ bool wide_loads(const DistillArgs& a) {
 
 template <typename T>
 cudaError_t launch_rows(int device, bool grad, DistillArgs& a, cudaStream_t s) {
-  // Parts of at most 32768 elements (with a gradient, so that a part is still in L2 when it
-  // comes again) or 65536; smaller ones for few rows, while the GPU has not
-  // kRowBlocks CTAs an SM and parts stay above kPartLeast.
+  // Parts of at most 32768 elements (with a gradient: a part comes again, from L2 if it is
+  // short enough) or 65536, as long as kMaxCluster of them hold the row, longer ones beyond;
+  // smaller ones for few rows, while the GPU has not kRowBlocks CTAs an SM and parts stay
+  // above kPartLeast.
   int log_ctas = 0;
   while ((1 << log_ctas) < kMaxCluster && (a.V >> log_ctas) > (grad ? 32768 : 65536)) ++log_ctas;
   while ((1 << log_ctas) < kMaxCluster && ((int64_t)a.N << log_ctas) < kRowBlocks * sm_count(device) &&

@@ -3,8 +3,13 @@
 // Both are bound by HBM traffic. A thread takes units of 8 elements, so that a warp's codes
 // are whole 128-byte lines and its 16-bit values whole 512-byte ones; a team of lanes (a
 // warp, or less for short rows) takes a piece of a row, kBatch loads of each lane in flight.
-// Measured at 128256 x 4096 (HBM bytes over time): bf16 to MX 219 us, 6.1 TB/s, to NV 270 us;
-// fp32 to MX 326 us, 7.3 TB/s; MX or NV to bf16 208 us, 6.4 TB/s, to fp32 425 us, 5.6 TB/s.
+// Measured at 128256 x 4096 (HBM bytes over time): bf16 to MX 219 us, 6.1 TB/s, to NV 272 us,
+// 4.9 TB/s (every lane of a block finds its scale: a division, two conversions and a
+// reciprocal for 8 elements, where MX has a shift); fp32 to MX 326 us, 7.3 TB/s; MX or NV to
+// bf16 208 us, 6.4 TB/s, to fp32 425 us, 5.6 TB/s. By id, to bf16: 1 row 2.2 us, 4096 random
+// ones 9.8 us (NV 10.3), 65536 121 us. A row's scales lie 512 bytes apart, as the product wants
+// them, so that 4096 random rows read 18.8 MB (MX) or 29.4 MB (NV) from HBM for 8.9 or 9.4 MB
+// of codes and scales.
 // 16-bit types are nearly bound by instructions (the conversions run at a quarter of the
 // rate): checking every unit's place in its row took 10 % more.
 #include <cmath>

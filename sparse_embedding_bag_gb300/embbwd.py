@@ -331,7 +331,8 @@ def emb_shard_status(shard):
     return load().emb_shard_status(shard)
 
 
-# ---- vocabulary operators (vocab.py calls these with tensors checked and outputs made)
+# ---- vocabulary operators: the plain binding, as of every call above. vocab.py checks tensors,
+# makes outputs and calls the same functions in a compiled entry, at a third of the host time.
 
 def emb_logits_process(device, logits, logits_dtype, logits_stride, B, V, prompt_ids, prompt_offsets,
                        prompt_n, output_ids, output_offsets, output_n, repetition, frequency,
