@@ -316,8 +316,8 @@ __device__ __forceinline__ void store_box_plain(uint16_t* out, int64_t stride, i
 //   load(maps, k, base, bar, rank), a_desc/b_desc(base), a_step, b_step, idesc
 //   store(maps, tmem, warp (0..3), lane, rank, aside, ok, zero)   lane `lane` of the warp holds a row
 // With kChunk an accumulator sums kChunk stages, and the epilogue's groups add these sums in registers,
-// half of the columns each:
-//   finish(sums, group, warp, lane, rank, ok)
+// half of the columns each (zeros of a tile without stages):
+//   finish(maps, sums, group, warp, lane, rank, aside, ok)
 template <typename Policy, bool kPair>
 __global__ void __launch_bounds__(kMmThreads, 1)
     k_entropy_mm(const __grid_constant__ Maps maps, const __grid_constant__ typename Policy::Args args) {
@@ -430,27 +430,33 @@ __global__ void __launch_bounds__(kMmThreads, 1)
       else
         mbar_arrive(smem_u32(&ctl.acc_empty[i & 1]));
     };
+    uint8_t* aside = smem_raw + (stages - smem_u32(smem_raw)) + kStages * S::kStage + warp * S::kAside;
     if constexpr (Policy::kChunk > 0) {
+      constexpr int kHalf = S::kCols / 2;
       while (p.next()) {
-        float v[128];
-        for (int32_t left = p.k_stages(); left > 0; left -= Policy::kChunk, ++j) {
-          filled(j);
-          const bool first = left == p.k_stages();
+        float v[kHalf];
+        const int32_t n = p.k_stages();
+        if (n == 0) {
 #pragma unroll
-          for (int q = 0; q < 128; q += 16) {
+          for (int i = 0; i < kHalf; ++i) v[i] = 0.f;
+        }
+        for (int32_t left = n; left > 0; left -= Policy::kChunk, ++j) {
+          filled(j);
+          const bool first = left == n;
+#pragma unroll
+          for (int q = 0; q < kHalf; q += 16) {
             if (!ok) break;
             float x[16];
-            tmem_load16(tmem + (j & 1) * S::kCols + group * 128 + q + lanes, x);
+            tmem_load16(tmem + (j & 1) * S::kCols + group * kHalf + q + lanes, x);
             tmem_load_wait();
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[q + i] = first ? x[i] : v[q + i] + x[i];
           }
           emptied(j);
         }
-        p.finish(v, group, warp & 3, lane, rank, ok);
+        p.finish(maps, v, group, warp & 3, lane, rank, aside, ok || n == 0);
       }
     } else {
-      uint8_t* aside = smem_raw + (stages - smem_u32(smem_raw)) + kStages * S::kStage + warp * S::kAside;
       for (uint32_t i = 0; p.next(); ++i) {
         if (p.k_stages() == 0) {
           if ((i & 1) == group) p.store(maps, tmem, warp & 3, lane, rank, aside, false, true);
@@ -505,24 +511,28 @@ struct LogitArgs {
   uint32_t* status;
 };
 
+constexpr int32_t kMostPlain = 8192;  // elements of fp16 rows whose gradients take logits of one sum
+
 // Tiles run over the tokens first: the hidden states stay in L2, the table is read once.
-enum LogitKind { kSums, kLongSums, kGradient };
+enum LogitKind { kSums, kLongSums, kGradient, kLongGradient };
 template <typename T, bool kPair, LogitKind kKind>
 struct Logits {
   using Args = LogitArgs;
-  using S = Shape<kPair, 256, kKind == kGradient ? 4096 : 0>;
+  static constexpr bool kOfGradient = kKind == kGradient || kKind == kLongGradient;
+  using S = Shape<kPair, 256, kOfGradient ? 4096 : 0>;
   // The tensor cores cut what an accumulator cannot hold, towards zero, at every 16 elements: sums
   // over 4096 elements gave losses 0.9e-6 off, over 8192 2.7e-6. Wider rows (kLongSums) are
   // summed 2048 elements at a time. (Up to there each group of warps takes a whole tile: 271 tokens,
-  // 50001 x 1031, 45 us instead of 58. Gradients, rounded to 16 bits, do not show it.)
-  static constexpr int kChunk = kKind == kLongSums ? 32 : 0;
+  // 50001 x 1031, 45 us instead of 58.) Logits of 15 in fp16 gradients show it from 8192 elements on: up to there
+  // 0.00021 of the norm became 0.00023, at 32768 0.00044 (kLongGradient: 0.00021). bf16 ones do not.
+  static constexpr int kChunk = kKind == kLongSums || kKind == kLongGradient ? 32 : 0;
   const Args& a;
   uint32_t m_tiles, step, t, tiles;  // fewer than 2^29: divisions of 32 bits, between two tiles' MMAs
   int32_t count, m, n;
   __device__ Logits(const Args& args, int32_t group, int32_t groups) : a(args), step(groups) {
     if (!a.count) pdl_trigger();  // the losses' kernel has work that does not wait for the tiles
     count = a.count ? *a.count : a.N;
-    m_tiles = ((kKind == kGradient ? rows_of_g(count, a.second) : count) + S::kRows - 1) / S::kRows;
+    m_tiles = ((kOfGradient ? rows_of_g(count, a.second) : count) + S::kRows - 1) / S::kRows;
     tiles = m_tiles * (uint32_t)((a.V1 - a.V0 + a.cols - 1) / a.cols);
     t = (uint32_t)(group - groups);
   }
@@ -550,17 +560,45 @@ struct Logits {
     const int64_t at = (a.targets ? a.targets[row] : (int64_t)a.target[row]) - v0;
     return at >= 0 && at < cols ? (int32_t)at : -1;
   }
+  // What a lane needs to know of its row of the tile to make it G.
+  struct Row {
+    int32_t row, cols, hit;
+    bool left, part;
+    float z_hit;
+    float2 par;
+  };
+  __device__ Row row_of(uint32_t warp, uint32_t lane, uint32_t rank) const {
+    Row r;
+    r.row = m * S::kRows + (int32_t)(rank * 128 + warp * 32 + lane);
+    r.left = a.second && r.row >= a.second;
+    const int32_t token = r.left ? r.row - a.second : r.row, v0 = a.V0 + n * a.cols;
+    r.part = token < count;
+    r.cols = min(a.cols, a.V1 - v0), r.hit = target_in_tile(token, v0, r.cols);
+    r.z_hit = r.part ? a.at_target[token] : 0.f;
+    r.par = r.part ? a.par[token] : make_float2(0.f, 0.f);
+    return r;
+  }
+  // Columns c..c+63 of the tile, as G.
+  __device__ void leave(const Maps& maps, const Row& r, float (&v)[2][32], int32_t c, uint32_t lane, uint8_t* aside, bool ok) const {
+#pragma unroll
+    for (int i = 0; i < 64; ++i) {
+      float& x = v[i / 32][i % 32];
+      const bool here = r.hit - c == i;
+      float p = ex2(fmaf(here ? r.z_hit : x, kLog2e, -r.par.x));
+      if (here) p -= 1.f;
+      x = !r.part || c + i >= r.cols ? 0.f : ok ? p * r.par.y : NAN;
+    }
+    if (r.left) {  // all lanes of a warp, or none
+#pragma unroll
+      for (int i = 0; i < 64; ++i) v[i / 32][i % 32] -= Elem<T>::get(Elem<T>::put(v[i / 32][i % 32]));
+    }
+    store_box<T>(&maps.out, n * a.cols + c, r.row - (int32_t)lane, aside, lane, v);
+  }
   // A thread holds a token's row of the tile.
   __device__ void store(const Maps& maps, uint32_t tmem, uint32_t warp, uint32_t lane, uint32_t rank, uint8_t* aside, bool ok,
                         bool) const {
-    const int32_t row = m * S::kRows + (int32_t)(rank * 128 + warp * 32 + lane);
-    const bool left = kKind == kGradient && a.second && row >= a.second;
-    const int32_t token = left ? row - a.second : row;
-    const bool part = token < count;
-    const int32_t v0 = a.V0 + n * a.cols, cols = min(a.cols, a.V1 - v0), hit = target_in_tile(token, v0, cols);
-    if (kKind == kGradient) {
-      const float z_hit = part ? a.at_target[token] : 0.f;
-      const float2 par = part ? a.par[token] : make_float2(0.f, 0.f);
+    if constexpr (kOfGradient) {
+      const Row r = row_of(warp, lane, rank);
 #pragma unroll 1
       for (int32_t c = 0; c < a.cols; c += 64) {
         float v[2][32];
@@ -570,22 +608,13 @@ struct Logits {
           tmem_load32(tmem + c + 32, v[1]);
           tmem_load_wait();
         }
-#pragma unroll
-        for (int i = 0; i < 64; ++i) {
-          float& x = v[i / 32][i % 32];
-          const bool here = hit - c == i;
-          float p = ex2(fmaf(here ? z_hit : x, kLog2e, -par.x));
-          if (here) p -= 1.f;
-          x = !part || c + i >= cols ? 0.f : ok ? p * par.y : NAN;
-        }
-        if (left) {  // all lanes of a warp, or none
-#pragma unroll
-          for (int i = 0; i < 64; ++i) v[i / 32][i % 32] -= Elem<T>::get(Elem<T>::put(v[i / 32][i % 32]));
-        }
-        store_box<T>(&maps.out, n * a.cols + c, row - (int32_t)lane, aside, lane, v);
+        leave(maps, r, v, c, lane, aside, ok);
       }
       return;
     }
+    const int32_t row = m * S::kRows + (int32_t)(rank * 128 + warp * 32 + lane);
+    const bool part = row < count;
+    const int32_t v0 = a.V0 + n * a.cols, cols = min(a.cols, a.V1 - v0), hit = target_in_tile(row, v0, cols);
     float ref = -INFINITY, sum = 0.f;
 #pragma unroll 1
     for (int32_t c = 0; c < cols && ok; c += 32) {
@@ -611,7 +640,21 @@ struct Logits {
     if (part) a.partial[(int64_t)n * a.cap + row] = make_float2(ref, ok ? sum : NAN);
   }
   // Half of the tile's columns, from registers.
-  __device__ void finish(float (&v)[128], uint32_t group, uint32_t warp, uint32_t lane, uint32_t rank, bool ok) const {
+  __device__ void finish(const Maps& maps, float (&v)[128], uint32_t group, uint32_t warp, uint32_t lane, uint32_t rank,
+                         uint8_t* aside, bool ok) const {
+    if constexpr (kOfGradient) {
+      const Row r = row_of(warp, lane, rank);
+#pragma unroll
+      for (int c = 0; c < 128; c += 64) {
+        const int32_t at = (int32_t)group * 128 + c;
+        if (at >= a.cols) continue;
+        float x[2][32];
+#pragma unroll
+        for (int i = 0; i < 64; ++i) x[i / 32][i % 32] = v[c + i];
+        leave(maps, r, x, at, lane, aside, ok);
+      }
+      return;
+    }
     const int32_t row = m * S::kRows + (int32_t)(rank * 128 + warp * 32 + lane);
     const int32_t v0 = a.V0 + n * a.cols + (int32_t)group * 128;
     const int32_t cols = min(a.cols - (int32_t)group * 128, a.V1 - v0), hit = target_in_tile(row, v0, cols);
@@ -730,16 +773,23 @@ __global__ void __launch_bounds__(kLossWarps * 32) k_entropy_loss(LossArgs a) {
 
 // ---- gradients of a piece of the vocabulary
 
+// Elements that an accumulator of a gradient sums at most. At every 16 elements the tensor cores cut the sum and the
+// products towards zero, by 2 to 4 times 2^-24 of the sum (measured; most where all products have one sign), so
+// that a sum that grows evenly over n elements lacks up to n / 16 * 2^-23: 2^20 tokens in one accumulator lacked
+// 2^-8. So many elements cost an eighth of the output's half step (2^-14 of the sum in fp16, 2^-11 in bf16).
+__host__ __device__ constexpr int32_t most_summed(bool fp16) { return fp16 ? 1 << 13 : 1 << 16; }
+
 // dh is summed over the vocabulary in `splits` parts; a part's fp32 sums lie at [part][packed
 // row][Dp]. Beside dW, whose tiles fill up the launch: enough parts that every CTA group has
 // one when there are few tokens. Alone: as many as leave the last round of the groups fullest (4096
 // tokens, 32768 x 4096: 2 parts 3.4 rounds of 4, 95 % full; 1 part 84 %), in two rounds or of
 // two parts at most. A part has four stages or more, for its way out and back costs as much (100
-// tokens, 5000 x 304, dh alone: 25 us, 33 with single stages).
+// tokens, 5000 x 304, dh alone: 25 us, 33 with single stages), and most_summed() elements or fewer.
 struct SplitArgs {
   int32_t d_tiles, Dp;
   bool alone;
   int32_t most;       // parts of four stages in the first piece
+  int32_t least;      // parts of most_summed() elements in it
 };
 template <bool kPair>
 using GradShape = Shape<kPair, kPair ? 256 : 128, 4096>;
@@ -753,6 +803,7 @@ __host__ __device__ inline int32_t splits_of(const SplitArgs& a, int32_t count, 
     const int32_t one_rounds = (one * tiles + groups - 1) / groups, two_rounds = (two * tiles + groups - 1) / groups;
     best = two * one_rounds > one * two_rounds ? two : one;
   }
+  if (best < a.least) best = a.least;
   return best < a.most ? best : a.most;
 }
 
@@ -770,10 +821,11 @@ struct GradArgs {
 };
 
 // The long sums (dh) come first, one or more a group; groups that have one fewer take
-// as many more tiles of dW first as that sum is long, the rest goes round.
-template <typename T, bool kPair>
+// as many more tiles of dW first as that sum is long, the rest goes round. kLong: sums over more than
+// most_summed() tokens, added up in registers.
+template <typename T, bool kPair, bool kLong>
 struct Grads {
-  static constexpr int kChunk = 0;
+  static constexpr int kChunk = kLong ? most_summed(std::is_same<T, __half>::value) / kDepth : 0;
   using Args = GradArgs;
   using S = GradShape<kPair>;
   static constexpr int32_t kCols = S::kCols;
@@ -851,14 +903,41 @@ struct Grads {
   __device__ uint32_t b_step() const { return 128; }
   __device__ uint32_t idesc() const { return idesc16<T>(S::kRows, width()) | (over_tokens ? 1u << 15 : 0u) | 1u << 16; }
 
+  // A lane's row of the tile, in the output of that row, and columns of the tile that there are.
+  __device__ int32_t row_of(uint32_t warp, uint32_t lane, uint32_t rank) const { return row0 + (int32_t)(rank * 128 + warp * 32 + lane); }
+  __device__ int32_t cols() const { return min(kCols, (over_tokens ? a.D : a.split.Dp) - col0); }
+  // Columns c..c+63 of the tile.
+  __device__ void leave(const Maps& maps, float (&v)[2][32], int32_t row, int32_t c, uint32_t lane, uint8_t* aside) const {
+    if (!over_tokens) {  // Dp is a multiple of 64
+      float* acc = a.acc + ((int64_t)part * pad + row) * a.split.Dp + col0 + c;
+#pragma unroll
+      for (int i = 0; i < 64; i += 4) {
+        float4* at = reinterpret_cast<float4*>(acc + i);
+        const float* e = &v[i / 32][i % 32];
+        float4 x = make_float4(e[0], e[1], e[2], e[3]);
+        if (!a.first) {
+          const float4 y = *at;
+          x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+        }
+        *at = x;
+      }
+      return;
+    }
+    const float back = a.scale[1];
+#pragma unroll
+    for (int i = 0; i < 64; ++i) v[i / 32][i % 32] *= back;
+    const int64_t first = a.V0 + row - (int32_t)lane;
+    if (a.wide)
+      store_box<T>(&maps.out, col0 + c, (int32_t)first, aside, lane, v);
+    else
+      store_box_plain<T>(static_cast<uint16_t*>(a.dtable) + first * a.dtable_stride + col0 + c, a.dtable_stride,
+                         a.V1 - (int32_t)first, cols() - c, aside, lane, v);
+  }
   __device__ void store(const Maps& maps, uint32_t tmem, uint32_t warp, uint32_t lane, uint32_t rank, uint8_t* aside, bool ok,
                         bool zero) const {
-    const int32_t row = row0 + (int32_t)(rank * 128 + warp * 32 + lane);
-    const float back = a.scale[1];
-    const int32_t cols = min(kCols, (over_tokens ? a.D : a.split.Dp) - col0);
-    float* acc = a.acc + ((int64_t)part * pad + row) * a.split.Dp + col0;
+    const int32_t row = row_of(warp, lane, rank), there = cols();
 #pragma unroll 1
-    for (int32_t c = 0; c < cols; c += 64) {
+    for (int32_t c = 0; c < there; c += 64) {
       float v[2][32];
       __syncwarp();
       if (ok) {
@@ -869,29 +948,20 @@ struct Grads {
 #pragma unroll
         for (int i = 0; i < 64; ++i) v[i / 32][i % 32] = zero ? 0.f : NAN;
       }
-      if (!over_tokens) {  // Dp is a multiple of 64
+      leave(maps, v, row, c, lane, aside);
+    }
+  }
+  // Half of the tile's columns, from registers.
+  __device__ void finish(const Maps& maps, float (&v)[kCols / 2], uint32_t group, uint32_t warp, uint32_t lane, uint32_t rank,
+                         uint8_t* aside, bool ok) const {
+    const int32_t row = row_of(warp, lane, rank), first = (int32_t)group * (kCols / 2), there = cols();
 #pragma unroll
-        for (int i = 0; i < 64; i += 4) {
-          float4* at = reinterpret_cast<float4*>(acc + c + i);
-          const float* e = &v[i / 32][i % 32];
-          float4 x = make_float4(e[0], e[1], e[2], e[3]);
-          if (!a.first) {
-            const float4 y = *at;
-            x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
-          }
-          *at = x;
-        }
-        continue;
-      }
+    for (int c = 0; c < kCols / 2; c += 64) {
+      if (first + c >= there) continue;
+      float x[2][32];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) v[i / 32][i % 32] *= back;
-      if (a.wide) {
-        store_box<T>(&maps.out, col0 + c, a.V0 + row - (int32_t)lane, aside, lane, v);
-      } else {
-        const int64_t first = a.V0 + row - (int32_t)lane;
-        store_box_plain<T>(static_cast<uint16_t*>(a.dtable) + first * a.dtable_stride + col0 + c, a.dtable_stride,
-                           a.V1 - (int32_t)first, cols - c, aside, lane, v);
-      }
+      for (int i = 0; i < 64; ++i) x[i / 32][i % 32] = ok ? v[c + i] : NAN;
+      leave(maps, x, row, first + c, lane, aside);
     }
   }
 };
@@ -977,7 +1047,7 @@ int32_t tile_columns(int64_t N, int32_t V, bool pair, int32_t groups, int32_t un
   return cols < 256 ? (int32_t)cols : 256;
 }
 
-Layout layout(int device, int64_t N, int32_t V, int32_t D, const void* table, int64_t stride, int gradients) {
+Layout layout(int device, int64_t N, int32_t V, int32_t D, const void* table, int64_t stride, int gradients, bool fp16) {
   Layout l{};
   l.cap = N > 0 ? (N + 255) / 256 * 256 : 256;
   l.Dp = (D + 63) / 64 * 64;  // whole lines: boxes of 128 bytes that straddle them cost twice
@@ -991,7 +1061,11 @@ Layout layout(int device, int64_t N, int32_t V, int32_t D, const void* table, in
   l.cols = tile_columns(N, V, l.pair, l.groups, l.pair ? 32 : 16);
   l.v_tiles = (V + l.cols - 1) / l.cols;
   l.padded = !readable(table, stride, V, D);
-  const int64_t whole = (int64_t)(V + 255) / 256, most = kPieceBytes / (l.cap * 2 * 256);
+  // A piece's G, and (fp16, of whose sums there are more) half as much for the parts of dh, two at least.
+  const int64_t rows = l.pair ? 256 : 128, m = N > 0 ? (N + rows - 1) / rows : 1, part = m * rows * l.Dp * 4;
+  const int64_t whole = (int64_t)(V + 255) / 256, fit = kPieceBytes / 2 / part;
+  int64_t most = kPieceBytes / (l.cap * 2 * 256);
+  if (fp16 && most > (fit > 2 ? fit : 2) * (most_summed(true) / 256)) most = (fit > 2 ? fit : 2) * (most_summed(true) / 256);
   const int64_t pieces = most < 1 ? whole : (whole + most - 1) / most;
   l.piece = (whole + pieces - 1) / pieces * 256;
   int64_t at = 0;
@@ -1008,8 +1082,10 @@ Layout layout(int device, int64_t N, int32_t V, int32_t D, const void* table, in
   if (gradients) {
     l.g = take(l.cap * l.piece * 2);
     // parts of dh: what splits_of() gives, for any number of packed rows
-    const int64_t rows = l.pair ? 256 : 128, m = N > 0 ? (N + rows - 1) / rows : 1, few = (2 * (int64_t)l.groups + l.d_tiles - 1) / l.d_tiles;
-    l.acc = take((few > 2 * m ? few : 2 * m) * rows * l.Dp * 4);
+    const int64_t few = (2 * (int64_t)l.groups + l.d_tiles - 1) / l.d_tiles * (rows * l.Dp * 4);
+    const int64_t first = V < l.piece ? V : l.piece, parts = (first + most_summed(fp16) - 1) / most_summed(fp16);
+    const int64_t long_sums = (parts > 2 ? parts : 2) * part;
+    l.acc = take(few > long_sums ? few : long_sums);
   }
   l.total = at;
   return l;
@@ -1122,7 +1198,9 @@ cudaError_t run(const Call& c, const Layout& l) {
     e = half_matrix_map(&grad_maps.out, c.dtable, c.V, c.D, c.V == 1 ? l.Dp : c.dtable_stride, 32);
   if (e != cudaSuccess) return e;
   const int64_t first = c.V < l.piece ? c.V : l.piece;
-  const SplitArgs split{l.d_tiles, Dp, !c.dtable, (int32_t)((first + 4 * kDepth - 1) / (4 * kDepth))};
+  constexpr bool kHalf = std::is_same<T, __half>::value;
+  const SplitArgs split{l.d_tiles, Dp, !c.dtable, (int32_t)((first + 4 * kDepth - 1) / (4 * kDepth)),
+                        (int32_t)((first + most_summed(kHalf) - 1) / most_summed(kHalf))};
   GradArgs ga{count, l.second, c.D, 0, 0, c.dhidden != nullptr, c.dtable != nullptr, true, wide, split,
               reinterpret_cast<float*>(w + l.acc), c.dtable, c.dtable_stride, scale, c.status};
   // G leaves in boxes of 64 columns
@@ -1133,8 +1211,20 @@ cudaError_t run(const Call& c, const Layout& l) {
     la.V0 = ga.V0 = (int32_t)v;
     la.V1 = ga.V1 = (int32_t)(v + l.piece < c.V ? v + l.piece : c.V);
     ga.first = v == 0;
-    e = launch_mm<Logits<T, kPair, kGradient>, kPair>(c.device, l.groups, logit_maps, la, c.s);
-    if (e == cudaSuccess) e = launch_mm<Grads<T, kPair>, kPair>(c.device, l.groups, grad_maps, ga, c.s);
+    if constexpr (kHalf)
+      e = c.D > kMostPlain ? launch_mm<Logits<T, kPair, kLongGradient>, kPair>(c.device, l.groups, logit_maps, la, c.s)
+                           : launch_mm<Logits<T, kPair, kGradient>, kPair>(c.device, l.groups, logit_maps, la, c.s);
+    else
+      e = launch_mm<Logits<T, kPair, kGradient>, kPair>(c.device, l.groups, logit_maps, la, c.s);
+    if (e != cudaSuccess) return e;
+    if constexpr (kPair) {
+      if (c.dtable && N > most_summed(kHalf)) {
+        e = launch_mm<Grads<T, true, true>, true>(c.device, l.groups, grad_maps, ga, c.s);
+        if (e != cudaSuccess) return e;
+        continue;
+      }
+    }
+    e = launch_mm<Grads<T, kPair, false>, kPair>(c.device, l.groups, grad_maps, ga, c.s);
     if (e != cudaSuccess) return e;
   }
   if (c.dhidden) {
@@ -1168,7 +1258,7 @@ emb_status cross_entropy(Call c, int64_t workspace_bytes, bool gradients) {
       (c.dhidden && (c.dhidden == c.table || c.dhidden == c.hidden)))
     return EMB_ERR_INVALID_ARG;
   if (c.V == 1) c.table_stride = c.dtable_stride = c.D;
-  const Layout l = layout(c.device, c.N, c.V, c.D, c.table, c.table_stride, gradients);
+  const Layout l = layout(c.device, c.N, c.V, c.D, c.table, c.table_stride, gradients, c.dtype == EMB_F16);
   if (workspace_bytes < l.total) return EMB_ERR_INVALID_ARG;
   return on_device(c.device, [&] {
     if (c.N == 0)
@@ -1186,7 +1276,9 @@ using namespace embbwd;
 extern "C" int64_t emb_cross_entropy_workspace(int device, int64_t N, int32_t V, int32_t D, const void* table,
                                                int64_t table_stride, int gradients) {
   if (!sizes_ok(device, N, V, D)) return -1;
-  return layout(device, N, V, D, table, table_stride, gradients).total;
+  const int64_t fp16 = layout(device, N, V, D, table, table_stride, gradients, true).total;
+  const int64_t bf16 = layout(device, N, V, D, table, table_stride, gradients, false).total;
+  return fp16 > bf16 ? fp16 : bf16;
 }
 
 extern "C" emb_status emb_cross_entropy_forward(int device, const void* hidden, emb_dtype dtype, int64_t hidden_stride,
