@@ -25,8 +25,9 @@ malformed offsets, 4: a bounded wait of a product ran out, and what was not fini
 caller clears it.
 
 Of these ``distill_loss``, ``rms_norm``, ``dropout`` and ``cross_entropy_loss`` take part in autograd, all but
-``dropout`` once (second derivatives are refused). The other calls take tensors that require
-gradients as values, and what they return has no history. An ``out`` counts as changed in place.
+``dropout`` once (second derivatives are refused) and in backward mode alone (tangents are refused). The other
+calls take tensors that require gradients, or carry tangents, as values, and what they return has no history. An
+``out`` counts as changed in place.
 """
 from __future__ import annotations
 
@@ -34,6 +35,7 @@ import ctypes
 import dataclasses
 
 import torch
+from torch.autograd import forward_ad
 
 from . import embbwd as E
 
@@ -254,6 +256,7 @@ class _Dropout(torch.autograd.Function):
         ctx.p, ctx.seed = p, seed
         if isinstance(call, torch.Tensor):
             ctx.save_for_backward(call)  # advanced before the backward: an error
+            ctx.save_for_forward(call)
             ctx.call = None
         else:
             ctx.call = call
@@ -266,16 +269,29 @@ class _Dropout(torch.autograd.Function):
         dx = dropout(_rows(grad), ctx.p, ctx.seed, call) if ctx.needs_input_grad[0] else None
         return dx, None, None, None, grad if ctx.summed else None
 
+    @staticmethod
+    def jvp(ctx, dx, _p, _seed, _call, dres):
+        call = ctx.saved_tensors[0] if ctx.call is None else ctx.call
+        if dx is None:
+            return dres.clone()
+        return dropout(_rows(dx), ctx.p, ctx.seed, call, residual=None if dres is None else _rows(dres))
+
+
+def _dual():
+    """Whether tensors may carry tangents (which `requires_grad` does not tell)."""
+    return getattr(forward_ad, "_current_level", 0) >= 0
+
 
 def dropout(x, p, seed, call=0, *, residual=None, out=None):
     """x [N, D] with each element kept and divided by 1 - p, or zero with probability p, plus residual.
 
     The elements kept depend on ``seed`` (0 to 2^64 - 1) and ``call``: an int, or an int64 CUDA tensor of one
     element that is read when the call runs, for captured graphs. Equal pairs keep equal elements, so a
-    program counts its calls. Differentiable unless ``out`` is given (which may be x or residual).
+    program counts its calls. Differentiable, in forward mode too, unless ``out`` is given (which may be x or
+    residual).
     """
-    if out is None and torch.is_grad_enabled() and (
-            getattr(x, "requires_grad", False) or getattr(residual, "requires_grad", False)):
+    if out is None and (_dual() or torch.is_grad_enabled() and (
+            getattr(x, "requires_grad", False) or getattr(residual, "requires_grad", False))):
         return _Dropout.apply(x, p, seed, call, residual)
     return (_entry or _native()).dropout(x, p, seed, call, residual, out)
 
