@@ -401,7 +401,8 @@ struct Weight {
   }
 };
 
-// x, weight, residual, eps, micro, out, sum_out -> (y, sum, rstd) or ((codes, scales), sum, None)
+// x, weight, residual, eps, micro, out, sum_out -> (y, sum, rstd) or ((codes, scales), sum, None). Without a sum
+// of its own the sum is x, or None where y has taken x's place.
 PyObject* rms_norm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return entry(n, 7, [&]() -> PyObject* {
     const Matrix x(a[0], "x");
@@ -432,7 +433,9 @@ PyObject* rms_norm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
           "emb_rms_norm_forward");
     if (y.defined()) written(y);
     if (sum.defined()) written(sum);
+    const bool gone = !sum.defined() && y.defined() && x.rows && y.data_ptr() == x.ptr();
     PyObject* first = micro ? pair(std::move(codes), std::move(scales)) : THPVariable_Wrap(std::move(y));
+    if (gone) return Py_BuildValue("(NON)", first, Py_None, THPVariable_Wrap(std::move(rstd)));
     if (micro) return Py_BuildValue("(NNO)", first, THPVariable_Wrap(sum.defined() ? sum : x.t), Py_None);
     return Py_BuildValue("(NNN)", first, THPVariable_Wrap(sum.defined() ? sum : x.t), THPVariable_Wrap(std::move(rstd)));
   });

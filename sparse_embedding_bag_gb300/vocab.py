@@ -193,7 +193,8 @@ def rms_norm_forward(x, weight=None, *, residual=None, eps=1e-6, format=None, ou
     """(y, sum, rstd fp32 [N]) of rows x [N, D]: y = sum * rstd * weight, sum = x + residual.
 
     weight [D] of any of the three types; residual [N, D] of x's type (without it ``sum`` is x itself, or
-    ``sum_out`` with its values). With format "mx8" y is a MicroMatrix and rstd None. ``out`` and ``sum_out`` may be x or residual.
+    ``sum_out`` with its values; None where ``out`` is x and no ``sum_out`` keeps them). With format "mx8" y is a
+    MicroMatrix and rstd None. ``out`` and ``sum_out`` may be x or residual.
     """
     if format not in (None, "mx8"):
         raise ValueError(f"format must be None or 'mx8', got {format!r}")
