@@ -422,7 +422,7 @@ PyObject* rms_norm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
       y = m.t, y_stride = m.stride;
       rstd = empty({x.rows}, at::kFloat, dev);  // for the gradient, which codes do not have
     }
-    if (res.p || a[6] != Py_None) {
+    if (a[2] != Py_None || a[6] != Py_None) {  // (rows that are none have no address)
       const Matrix m = new_or(x, a[6], "sum_out");
       sum = m.t, sum_stride = m.stride;
     }
