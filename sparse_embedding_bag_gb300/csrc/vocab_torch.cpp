@@ -564,11 +564,15 @@ PyObject* cross_entropy_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (a[3] == Py_None) refuse("lse must be given");
     const Gradient h(x.h, a[5], a[7], "out_hidden"), w(x.w, a[6], a[8], "out_table");
     if (!h.t.defined() && !w.t.defined()) refuse("no gradient is asked for");
-    const at::Tensor ws = x.workspace(true);
-    check(lib.cross_entropy_backward(dev, x.h.ptr(), x.h.dtype, x.h.stride, x.h.rows, x.w.ptr(), x.w.stride, x.V, x.D,
-                                     x.targets, x.of_rows(a[3], "lse"), x.of_rows(a[4], "row_weight"), h.p, h.stride, w.p,
-                                     w.stride, ws.data_ptr(), ws.numel(), status_word(a[9], dev), stream(dev)),
-          "emb_cross_entropy_backward");
+    const float *lse = x.of_rows(a[3], "lse"), *weight = x.of_rows(a[4], "row_weight");
+    uint32_t* const status = status_word(a[9], dev);
+    if (x.h.rows > 0 || w.t.defined()) {  // else there is nothing to write, and the hidden states' gradient has no address
+      const at::Tensor ws = x.workspace(true);
+      check(lib.cross_entropy_backward(dev, x.h.ptr(), x.h.dtype, x.h.stride, x.h.rows, x.w.ptr(), x.w.stride, x.V, x.D,
+                                       x.targets, lse, weight, h.p, h.stride, w.p, w.stride, ws.data_ptr(), ws.numel(),
+                                       status, stream(dev)),
+            "emb_cross_entropy_backward");
+    }
     return Py_BuildValue("(NN)", h.wrap(), w.wrap());
   });
 }

@@ -25,3 +25,23 @@ def test_dropout(V):  # noqa: F811
     x, r = (torch.empty((0, 40), device="cuda", requires_grad=True) for _ in range(2))
     V.dropout(x, 0.5, 1, residual=r).sum().backward()
     assert x.grad.shape == r.grad.shape == (0, 40)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_cross_entropy(V, dtype):  # noqa: F811
+    h = torch.empty((0, 64), device="cuda", dtype=dtype, requires_grad=True)
+    t = torch.randn((50, 64), device="cuda").to(dtype).requires_grad_()
+    at, lse = torch.empty(0, dtype=torch.int64, device="cuda"), torch.empty(0, device="cuda")
+    for table in (t, t.detach()):  # both gradients, the hidden states' alone
+        loss = V.cross_entropy_loss(h, table, at)
+        assert loss.shape == (0,)
+        h.grad = None
+        loss.sum().backward()
+        assert h.grad.shape == (0, 64)
+    assert not t.grad.any()
+    V.cross_entropy_loss(h.detach(), t, at).sum().backward()  # the table's alone
+    assert not t.grad.any()
+    dh, dt = V.cross_entropy_backward(h.detach(), t.detach(), at, lse, want_table=False)
+    assert dh.shape == (0, 64) and dt is None
+    with pytest.raises(ValueError):
+        V.cross_entropy_backward(h.detach(), t.detach(), at, torch.empty(1, device="cuda"), want_table=False)
