@@ -63,7 +63,7 @@ int dtype_code(at::ScalarType t) {
   return t == at::kFloat ? EMB_F32 : t == at::kHalf ? EMB_F16 : t == at::kBFloat16 ? EMB_BF16 : -1;
 }
 
-// A 2-D CUDA tensor whose rows are contiguous.
+// A 2-D CUDA tensor whose rows, if there are any, are contiguous.
 struct Matrix {
   at::Tensor t;
   int64_t rows, cols, stride;
@@ -74,7 +74,7 @@ struct Matrix {
     const int code = dtype_code(x.scalar_type());
     if (code < 0) refuse("%s must be float32, float16 or bfloat16", name);
     rows = x.size(0), cols = x.size(1), stride = x.stride(0);
-    if (cols > 1 && x.stride(1) != 1) refuse("the rows of %s must be contiguous", name);
+    if (rows > 0 && cols > 1 && x.stride(1) != 1) refuse("the rows of %s must be contiguous", name);
     dtype = (emb_dtype)code, device = x.get_device();
   }
   Matrix(PyObject* o, const char* name) : Matrix(tensor(o, name), name) {}

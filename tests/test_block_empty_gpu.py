@@ -45,3 +45,13 @@ def test_cross_entropy(V, dtype):  # noqa: F811
     assert dh.shape == (0, 64) and dt is None
     with pytest.raises(ValueError):
         V.cross_entropy_backward(h.detach(), t.detach(), at, torch.empty(1, device="cuda"), want_table=False)
+
+
+def test_broadcast_gradients_of_no_rows(V):  # noqa: F811
+    """An expanded tensor without elements counts as contiguous and keeps its strides of zero."""
+    none = torch.zeros((), device="cuda").expand(0, 40)
+    assert none.contiguous().stride() == (0, 0)
+    x, w = torch.empty((0, 40), device="cuda"), torch.ones(40, device="cuda")
+    dx, dw = V.rms_norm_backward(none, x, w, torch.empty(0, device="cuda"), grad_sum=none)
+    assert dx.shape == (0, 40) and not dw.any()
+    assert V.dropout(none, 0.5, 1).shape == V.rms_norm_forward(none)[0].shape == (0, 40)
