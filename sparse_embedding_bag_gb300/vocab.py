@@ -321,8 +321,9 @@ class _EntropyGradient(torch.autograd.Function):
     """The loss's gradients; their own derivatives are not built, and asking for them is an error."""
 
     @staticmethod
-    def forward(ctx, hidden, table, grad, targets, lse, want_hidden, want_table):
-        return cross_entropy_backward(hidden, table, targets, lse, grad, want_hidden=want_hidden, want_table=want_table)
+    def forward(ctx, hidden, table, grad, targets, lse, want_hidden, want_table, status):
+        return cross_entropy_backward(hidden, table, targets, lse, grad, want_hidden=want_hidden, want_table=want_table,
+                                      status=status)
 
     @staticmethod
     def backward(ctx, *grads):
@@ -331,18 +332,21 @@ class _EntropyGradient(torch.autograd.Function):
 
 class _EntropyLoss(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, hidden, table, targets):
-        loss, lse = cross_entropy_forward(hidden, table, targets)
+    def forward(ctx, hidden, table, targets, status):
+        loss, lse = cross_entropy_forward(hidden, table, targets, status=status)
         ctx.save_for_backward(hidden, table, targets, lse)
+        ctx.status = status  # collects bits, and may be cleared at any time: not a saved value
         return loss
 
     @staticmethod
     def backward(ctx, grad):
         hidden, table, targets, lse = ctx.saved_tensors
         want = ctx.needs_input_grad
-        return (*_EntropyGradient.apply(hidden, table, grad.float().contiguous(), targets, lse, want[0], want[1]), None)
+        return (*_EntropyGradient.apply(hidden, table, grad.float().contiguous(), targets, lse, want[0], want[1],
+                                        ctx.status), None, None)
 
 
-def cross_entropy_loss(hidden, table, targets):
-    """Differentiable loss [N] of hidden states against the table (once)."""
-    return _EntropyLoss.apply(hidden, table, targets)
+def cross_entropy_loss(hidden, table, targets, *, status=None):
+    """Differentiable loss [N] of hidden states against the table (once). ``status`` collects the error bits of the
+    forward and of the backward: a target beyond the table takes no part, and is only reported there."""
+    return _EntropyLoss.apply(hidden, table, targets, status)
