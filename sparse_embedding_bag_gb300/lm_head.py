@@ -69,29 +69,35 @@ def serve(table, layer, prompts, steps, *, format="nv", norm=None, mask=None, re
     return said.tolist()
 
 
-def gradients(table, layer, norm, tokens, targets, *, p, seed, call):
+def gradients(table, layer, norm, tokens, targets, *, p, seed, call, status=None):
     """(mean loss, gradients of the looked-up rows, the table as head, layer and norm) of one batch.
 
-    tokens, targets int64 [N] (targets negative: no part); table, layer and norm bf16 or fp16.
+    tokens, targets int64 [N] (targets negative: no part; beyond the table: none either, and an error bit in
+    ``status``); table, layer and norm bf16 or fp16. The mean is over the tokens that take part.
     """
     rows, head, layer, norm = (x.detach().requires_grad_() for x in (table[tokens], table, layer, norm))
     hidden = vocab.dropout(torch.tanh(rows @ layer), p, seed, call, residual=rows)
-    loss = vocab.cross_entropy_loss(vocab.rms_norm(hidden, norm), head, targets)
-    mean = loss.sum() / (targets >= 0).sum().clamp(min=1)
+    loss = vocab.cross_entropy_loss(vocab.rms_norm(hidden, norm), head, targets, status=status)
+    mean = loss.sum() / ((targets >= 0) & (targets < table.shape[0])).sum().clamp(min=1)
     return mean.detach(), torch.autograd.grad(mean, (rows, head, layer, norm))
 
 
 def train(table, layer, norm, tokens, targets, *, lr=1.0, steps=1, p=0.1, seed=0):
-    """``steps`` steps of next-token training on one batch, all in place; returns the mean loss of each."""
+    """``steps`` steps of next-token training on one batch, all in place; returns the mean loss of each.
+
+    A target beyond the table is an error, raised after the steps (they do not wait for the GPU).
+    """
     V, D = table.shape
     N = tokens.numel()
     dtype = E.EMB_BF16 if table.dtype == torch.bfloat16 else E.EMB_F16
     plan = E.emb_bwd_plan(table.device.index, 1, [0, V], [0, D], [0], None, dtype, dtype, N, 1)
     offsets = torch.tensor([0, N], device=table.device)
+    status = torch.zeros(1, dtype=torch.int32, device=table.device)
     losses = []
     try:
         for step in range(steps):
-            loss, (rows, head, d_layer, d_norm) = gradients(table, layer, norm, tokens, targets, p=p, seed=seed, call=step)
+            loss, (rows, head, d_layer, d_norm) = gradients(table, layer, norm, tokens, targets, p=p, seed=seed, call=step,
+                                                            status=status)
             losses.append(loss)
             table.sub_(head, alpha=lr)
             E.emb_nobag_bwd_sgd(plan, table, tokens, offsets, N, 1, rows, lr, E.EMB_NOBAG_SORTED)
@@ -100,6 +106,8 @@ def train(table, layer, norm, tokens, targets, *, lr=1.0, steps=1, p=0.1, seed=0
         st = E.emb_plan_status(plan)
         if st != E.EMB_OK:
             raise E.EmbError(st, "emb_nobag_bwd_sgd")
+        if status.item():
+            raise RuntimeError(f"device error bits {status.item()}")
     finally:
         E.emb_plan_destroy(plan)
     return [x.item() for x in losses]
