@@ -107,8 +107,8 @@ class _DistillGradient(torch.autograd.Function):
     """The loss's gradient; its own derivatives are not built, and asking for them is an error."""
 
     @staticmethod
-    def forward(ctx, logits, grad, teacher_ids, teacher_logits, stats, temperature):
-        return distill_backward(logits, teacher_ids, teacher_logits, stats, grad, temperature=temperature)
+    def forward(ctx, logits, grad, teacher_ids, teacher_logits, stats, temperature, status):
+        return distill_backward(logits, teacher_ids, teacher_logits, stats, grad, temperature=temperature, status=status)
 
     @staticmethod
     def backward(ctx, grad):
@@ -117,23 +117,24 @@ class _DistillGradient(torch.autograd.Function):
 
 class _DistillLoss(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, logits, teacher_ids, teacher_logits, temperature, teacher_lse):
+    def forward(ctx, logits, teacher_ids, teacher_logits, temperature, teacher_lse, status):
         loss, stats = distill_forward(logits, teacher_ids, teacher_logits, temperature=temperature,
-                                      teacher_lse=teacher_lse)
+                                      teacher_lse=teacher_lse, status=status)
         ctx.save_for_backward(logits, teacher_ids, teacher_logits, stats)
-        ctx.temperature = temperature
+        ctx.temperature, ctx.status = temperature, status
         return loss
 
     @staticmethod
     def backward(ctx, grad):
         logits, ids, teacher, stats = ctx.saved_tensors
-        return (_DistillGradient.apply(logits, grad.float().contiguous(), ids, teacher, stats, ctx.temperature), None,
-                None, None, None)
+        return (_DistillGradient.apply(logits, grad.float().contiguous(), ids, teacher, stats, ctx.temperature,
+                                       ctx.status), None, None, None, None, None)
 
 
-def distill_loss(logits, teacher_ids, teacher_logits, *, temperature=1.0, teacher_lse=None):
-    """Differentiable loss [N] of ``logits`` (once; the teacher takes no gradient)."""
-    return _DistillLoss.apply(logits, teacher_ids, teacher_logits, temperature, teacher_lse)
+def distill_loss(logits, teacher_ids, teacher_logits, *, temperature=1.0, teacher_lse=None, status=None):
+    """Differentiable loss [N] of ``logits`` (once; the teacher takes no gradient). ``status`` collects the error
+    bits of the forward and of the backward."""
+    return _DistillLoss.apply(logits, teacher_ids, teacher_logits, temperature, teacher_lse, status)
 
 
 @dataclasses.dataclass
