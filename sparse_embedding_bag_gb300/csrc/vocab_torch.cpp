@@ -5,7 +5,9 @@
 #include <Python.h>
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <ATen/record_function.h>
 #include <c10/core/GradMode.h>
+#include <c10/core/impl/LocalDispatchKeySet.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -133,9 +135,17 @@ at::ScalarType type_of(PyObject* o) {
   if (dtype_code(t) < 0) refuse("dtype must be float32, float16 or bfloat16");
   return t;
 }
-// Straight from the caching allocator (through the dispatcher an allocation takes twice as long).
+// Whether nothing between a call and the allocator has to see an allocation: no dispatch mode or transform, no
+// profiler, and no program that wants uninitialised memory filled.
+bool unseen() {
+  const at::Context& c = at::globalContext();
+  return (c10::impl::tls_local_dispatch_key_set().included_ - c10::default_included_set).empty() && !at::hasCallbacks() &&
+         !(c.deterministicAlgorithms() && c.deterministicFillUninitializedMemory());
+}
+// Then straight from the caching allocator: 0.3 us instead of 0.8 by the dispatcher (a norm of one row 5.0 us of host time instead of 6.5).
 at::Tensor empty(at::IntArrayRef size, at::ScalarType type, int device) {
-  return at::Tensor(at::detail::empty_cuda(size, type, at::Device(at::kCUDA, device), std::nullopt));
+  if (unseen()) return at::Tensor(at::detail::empty_cuda(size, type, at::Device(at::kCUDA, device), std::nullopt));
+  return at::empty(size, at::TensorOptions().dtype(type).device(at::kCUDA, device));
 }
 void* stream(int device) { return c10::cuda::getCurrentCUDAStream(device).stream(); }
 
