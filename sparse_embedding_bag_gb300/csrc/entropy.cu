@@ -107,9 +107,10 @@ __device__ __forceinline__ float dot_eight(const uint4& x, const uint4& y, float
 // D = 4096 some 3e-6 of a logit), which a loss that is the difference of two large numbers
 // would show; it takes the place of the tiles' own. Bound by latency: 6 us for 301 rows, 26 for 4096 of
 // 4096 elements (4 TB/s).
+constexpr int kPartSums = 8;
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_entropy_rows(RowArgs a) {
-  __shared__ float f_scratch[kWarps];
+  __shared__ float f_scratch[kWarps], sums[kWarps][kPartSums];
   __shared__ int32_t before_w[kWarps], all_w[kWarps], list[kThreads], goal[kThreads], rank_w[kWarps];
   pdl_wait();
   const int32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -171,12 +172,13 @@ __global__ void __launch_bounds__(kThreads) k_entropy_rows(RowArgs a) {
       a.par[n] = make_float2(a.lse ? a.lse[r] * kLog2e : 0.f, (a.weight ? a.weight[r] : 1.f) * scale);
     }
     __syncthreads();
-    // a block's warps share out its rows: few rows, several warps each
+    // a block's warps share out its rows: few rows, several warps each. However many take a row, its sum is that of
+    // kPartSums, each of every eighth 256 elements: its bits do not depend on which of its neighbours take part
     const int32_t row_warps = here <= 1 ? 8 : here <= 2 ? 4 : here <= 4 ? 2 : 1;
     const int32_t together = kWarps / row_warps, lanes = row_warps * 32, l = tid & (lanes - 1);
     for (int32_t j = 0; j < here; j += together) {
       const int32_t i = j + tid / lanes;
-      float z = 0.f;
+      float part_of[kPartSums] = {};
       if (i < here) {
         const uint16_t* from = static_cast<const uint16_t*>(a.hidden) + (int64_t)list[i] * a.stride;
         const uint16_t* with = static_cast<const uint16_t*>(a.table) + (int64_t)goal[i] * a.table_stride;
@@ -186,17 +188,28 @@ __global__ void __launch_bounds__(kThreads) k_entropy_rows(RowArgs a) {
           const uint4 u = load_eight(from, k, a.D);
           *reinterpret_cast<uint4*>(to + k) = u;
           if (a.second) *reinterpret_cast<uint4*>(to + (int64_t)a.second * a.Dp + k) = u;
-          z = dot_eight<T>(u, load_eight(with, k, a.D), z);
+          const float z = dot_eight<T>(u, load_eight(with, k, a.D), 0.f);
+          const int32_t own = k / 256 % kPartSums;
+#pragma unroll
+          for (int s = 0; s < kPartSums; ++s) part_of[s] += s == own ? z : 0.f;
         }
       }
-      z = warp_sum(z);
-      if (row_warps > 1) {
-        if (lane == 0) f_scratch[warp] = z;
+#pragma unroll
+      for (int s = 0; s < kPartSums; ++s) part_of[s] = warp_sum(part_of[s]);
+      if (row_warps > 1) {  // the others' parts are zeros here
+        if (lane == 0) {
+#pragma unroll
+          for (int s = 0; s < kPartSums; ++s)
+            if (s % row_warps == warp % row_warps) sums[warp / row_warps][s] = part_of[s];
+        }
         __syncthreads();
-        z = 0.f;
-        for (int w = 0; w < row_warps; ++w) z += f_scratch[warp / row_warps * row_warps + w];
+#pragma unroll
+        for (int s = 0; s < kPartSums; ++s) part_of[s] = sums[warp / row_warps][s];
         __syncthreads();
       }
+      float z = 0.f;
+#pragma unroll
+      for (int s = 0; s < kPartSums; ++s) z += part_of[s];
       if (i < here && l == 0) a.at_target[before + i] = z;
     }
     before += here;
