@@ -878,7 +878,7 @@ struct Grads {
       part = at / tiles_h;
       const int32_t t = at - part * tiles_h;
       to_tile(t);
-      k0 = (uint32_t)kh * part / splits, k1 = (uint32_t)kh * (part + 1) / splits;  // 2^14 stages, 2^8 parts at most
+      k0 = (uint32_t)kh * part / splits, k1 = (uint32_t)kh * (part + 1) / splits;  // 2^14 stages, 2^9 parts at most
       if (k0 < k1 || a.first) return true;  // else a part that a short last piece leaves empty
     }
     at += phase == 1 ? groups - rest : groups;
@@ -1151,8 +1151,8 @@ cudaError_t run(const Call& c, const Layout& l) {
 
   // The losses of few tokens need no packing: a row that takes no part is one more row of the tile.
   const bool direct = !gradients && !kPair && readable(c.hidden, c.hidden_stride, N, c.D);
-  // two blocks an SM and more
-  const int32_t per_block = N / 1024 > 8 ? N / 1024 : N < 304 ? 1 : N < 608 ? 2 : N < 1216 ? 4 : 8;
+  // two blocks an SM and more, up to eight rows each; 1024 blocks at most, for each scans all targets
+  const int32_t two = 2 * sm_count(c.device), per_block = N / 1024 > 8 ? N / 1024 : N < two ? 1 : N < 2 * two ? 2 : N < 4 * two ? 4 : 8;
   RowArgs rows{c.hidden, c.hidden_stride, N, c.D, c.V, c.targets, c.weight, c.lse,
                reinterpret_cast<uint16_t*>(w + l.rows), Dp, per_block, gradients, l.second,
                gradients && std::is_same<T, __half>::value, count, rank, c.table, c.table_stride, target, at_target, par, scale,
