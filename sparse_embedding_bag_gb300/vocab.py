@@ -279,11 +279,6 @@ class _Dropout(torch.autograd.Function):
         return dropout(_rows(dx), ctx.p, ctx.seed, call, residual=None if dres is None else _rows(dres))
 
 
-def _dual():
-    """Whether tensors may carry tangents (which `requires_grad` does not tell)."""
-    return getattr(forward_ad, "_current_level", 0) >= 0
-
-
 def dropout(x, p, seed, call=0, *, residual=None, out=None):
     """x [N, D] with each element kept and divided by 1 - p, or zero with probability p, plus residual.
 
@@ -292,7 +287,8 @@ def dropout(x, p, seed, call=0, *, residual=None, out=None):
     program counts its calls. Differentiable, in forward mode too, unless ``out`` is given (which may be x or
     residual).
     """
-    if out is None and (_dual() or torch.is_grad_enabled() and (
+    # tensors carry tangents while a dual level is open, which `requires_grad` does not tell
+    if out is None and (forward_ad._current_level >= 0 or torch.is_grad_enabled() and (
             getattr(x, "requires_grad", False) or getattr(residual, "requires_grad", False))):
         return _Dropout.apply(x, p, seed, call, residual)
     return (_entry or _native()).dropout(x, p, seed, call, residual, out)
