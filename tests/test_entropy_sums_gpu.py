@@ -2,9 +2,13 @@
 elements, by half a unit of its last place in the mean: at most 2^-24 of a sum that grows. Over n elements in one
 accumulator a gradient therefore comes out up to n / 16 * 2^-24 too small. Rounding errors of single elements have no
 direction; what all of a gradient lacks in common shows in its projection on the true one."""
+import ctypes
+
 import pytest
 
 import _block_ref as R
+from sparse_embedding_bag_gb300 import embbwd as E
+from test_entropy_gpu import impatient  # noqa: F401 (a fixture)
 from test_vocab_gpu import V  # noqa: F401 (a fixture)
 
 pytestmark = pytest.mark.gpu
@@ -96,3 +100,35 @@ def test_logits_of_wide_rows(V, N):  # noqa: F811
         common = 128 * 2.0 ** -24 * 16 * 1.01
         assert abs(lacking(dh, a)) <= common + noise(a, dtype, u * (a @ t.double().T))
         assert abs(lacking(dt, b)) <= common + noise(b, dtype, u * (h.double() @ b.T))
+
+
+@pytest.mark.parametrize("N,n_vocab,D", [(9000, 1200, 264), (300, 3000, 8256), (30, 5000, 8264)])
+def test_long_sums_that_give_up(V, impatient, N, n_vocab, D):  # noqa: F811
+    """As for short sums: an error bit, NaN where nothing was computed, and a GPU that carries on."""
+    vp, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+    f = impatient.emb_cross_entropy_step
+    f.argtypes = [i32, vp, i32, i64, i64, vp, i64, i32, i32, vp, vp, vp, vp, i64, vp, i64, vp, i64, vp, vp]
+    g = torch.Generator(device="cuda").manual_seed(N)
+    h = torch.randn((N, D), generator=g, device="cuda").half()
+    t = (torch.randn((n_vocab, D), generator=g, device="cuda") * D ** -0.5).half()
+    at = torch.randint(-1, n_vocab, (N,), generator=g, device="cuda")
+    want = V.cross_entropy_step(h, t, at)
+    need = E.emb_cross_entropy_workspace(0, N, n_vocab, D, t, D, 1)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    gave_up = 0
+    for _ in range(3):
+        loss, dh, dt = torch.full((N,), 7.0, device="cuda"), torch.full_like(h, 7.0), torch.full_like(t, 7.0)
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        assert f(0, h.data_ptr(), E.EMB_F16, D, N, t.data_ptr(), D, n_vocab, D, at.data_ptr(), None, loss.data_ptr(),
+                 dh.data_ptr(), D, dt.data_ptr(), D, ws.data_ptr(), need, status.data_ptr(),
+                 torch.cuda.current_stream().cuda_stream) == 0
+        missing = 0
+        for got, right in zip((loss, dh, dt), want):
+            nan = got.isnan()
+            missing += nan.sum().item()
+            assert torch.equal(torch.where(nan, right, got), right)
+        assert status.item() in (0, 4) and (missing > 0) <= (status.item() == 4)
+        gave_up += status.item() == 4
+    assert gave_up
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    assert all(torch.equal(a, b) for a, b in zip(V.cross_entropy_step(h, t, at, status=status), want)) and status.item() == 0
