@@ -491,7 +491,8 @@ emb_status emb_micro_matmul(int device, const uint8_t* x_codes, const uint8_t* x
  * grad_sum: the gradient that arrives at s by other ways, NULL = 0. out may be grad, sum or
  * grad_sum themselves (same stride). With grad_weight it needs a workspace (16-byte aligned, not
  * shared by calls that may run at once) of emb_rms_norm_workspace bytes (-1: sizes
- * out of range). The sums' order depends on the number of SMs alone. */
+ * out of range). The same call gives the same bits: the order of sums depends on the sizes, on
+ * where in 16 bytes rows lie and on the number of SMs, never on timing. */
 emb_status emb_rms_norm_forward(int device, const void* x, emb_dtype dtype, int64_t x_stride, int64_t N,
                                 int32_t D, const void* residual, int64_t residual_stride,
                                 const void* weight, emb_dtype weight_dtype, float eps, void* out,
@@ -528,9 +529,14 @@ emb_status emb_dropout(int device, const void* x, emb_dtype dtype, int64_t x_str
  * targets int64[N]. A row with a negative target takes no part: its loss, lse and grad_hidden
  * are 0, and nothing that it holds reaches another output. So does a target >= V, with error
  * bit 1. row_weight fp32[N] or NULL = 1; lse fp32[N] (may be NULL in the forward call). G is
- * rounded to hidden's type (fp16: scaled by a power of two, from the largest weight of a row that
- * takes part) before it is multiplied, up to 64 tokens to a sum of two such numbers; sums are
- * fp32, in a fixed order. Probabilities and products below 2^-126 may count as 0.
+ * rounded to hidden's type before it is multiplied, up to 64 tokens to a sum of two such numbers.
+ * (fp16: scaled by a power of two that brings the largest weight of a row that takes part to
+ * 2^14..2^15, so that probabilities down to 2^-28 keep all bits in a row of that weight, and
+ * down to 2^(k - 28) in one whose weight is 2^-k of it.) Sums are fp32, in a fixed order: the
+ * same call (sizes, places in 16 bytes, targets that take part, number of SMs) gives the same
+ * bits, and a row's loss and lse do not depend on the other rows' targets. An accumulator of a
+ * gradient sums 2^13 (fp16) or 2^16 (bf16) elements at most. Probabilities and products below
+ * 2^-126 may count as 0.
  *   emb_cross_entropy_forward    loss, lse
  *   emb_cross_entropy_backward   gradients from the forward's lse; the logits are computed
  *                                again. A NULL grad_hidden or grad_table is not computed
@@ -538,9 +544,12 @@ emb_status emb_dropout(int device, const void* x, emb_dtype dtype, int64_t x_str
  * With N = 0 grad_table is set to zero. The outputs must not overlap the inputs nor each
  * other. These calls
  * need a workspace (256-byte aligned, not shared by calls that may run at once) of
- * emb_cross_entropy_workspace bytes, for the same sizes, table pointer and stride;
- * gradients != 0 for the backward and the step (per token some V / 16 + 2 D bytes, with gradients up
- * to 10 D more, and 512 MB for a piece of G; a table off 16-byte boundaries is copied as well).
+ * emb_cross_entropy_workspace bytes, for the same sizes, table pointer and stride, either type;
+ * gradients != 0 for the backward and the step. With N rounded up to 256 and D to 64 it takes up
+ * to N (V / 16 + 2 D + 16 SMs + 64) bytes; with gradients also 2 N V or 512 MB for G, whichever is
+ * less (512 N at least), and for the parts of grad_hidden up to the largest of 8 N D, 256 MB,
+ * 24 KB for each column, and 256 KB for each SM + 1 KB for each column; a table that bulk copies
+ * cannot read (off 16-byte boundaries, or D not a multiple of 8) 2 V D more.
  * It returns -1 for sizes out of range. */
 int64_t emb_cross_entropy_workspace(int device, int64_t N, int32_t V, int32_t D, const void* table,
                                     int64_t table_stride, int gradients);

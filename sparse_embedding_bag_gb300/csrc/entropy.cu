@@ -9,14 +9,18 @@
 // taken in pieces; a piece's logits are computed again and leave as G in the operands' type
 // (Logits with kGradient), then one launch multiplies G with both sides (k_entropy_mm<Grads>):
 // the piece's rows of dW, whole sums over the tokens, and its part of dh, added to fp32 sums in
-// the workspace. The order of all sums is fixed.
+// the workspace. The order of all sums is fixed, and none stays in one accumulator for longer than
+// most_summed() elements.
 //
 // G is rounded to the operands' type because the tensor cores take two operands of one type.
 // bf16 keeps its range; fp16 is scaled by a power of two that brings the largest weight
-// to 2^14..2^15, so that probabilities down to 2^-29 keep all bits. Up to 64 tokens G is two such
+// to 2^14..2^15, so that probabilities down to 2^-28 keep all bits in a row of that weight, and down to
+// 2^(k - 28) in one whose weight is 2^-k of it (one scale for all rows: dW adds up rows). Gradients
+// then carry two roundings, 0.0024 of the norm in bf16 and 0.00030 in fp16 where one makes 0.0017 and
+// 0.00021. Up to 64 tokens G is two such
 // numbers, its rounding and what that leaves, in rows n and n + 64 (up to 32 tokens n + 32) of a tile, which no token fills:
 // with few tokens single roundings show in the gradients (5 % of the time at 128256 x 4096; two
-// tiles of 128 tokens would cost 33 %).
+// tiles of 128 tokens would cost 33 %; for all tokens both products of G, half of a step's time, would double).
 //
 // The products share one frame (k_entropy_mm): persistent CTAs, in pairs above 128 tokens
 // (tiles of up to 256 x 256, each CTA half of both operands), stages 64 elements deep by TMA in the
@@ -105,8 +109,8 @@ __device__ __forceinline__ float dot_eight(const uint4& x, const uint4& y, float
 // the rows that it copies), so that no launch has to come before. The logit of a row's
 // target is summed here by fp32 FMAs: the tensor cores' sums lose their last bits (at
 // D = 4096 some 3e-6 of a logit), which a loss that is the difference of two large numbers
-// would show; it takes the place of the tiles' own. Bound by latency: 6 us for 301 rows, 26 for 4096 of
-// 4096 elements (4 TB/s).
+// would show; it takes the place of the tiles' own. Bound by latency: 7 us for 301 rows, 32 for 4096 of
+// 4096 elements (2.1 TB/s of rows read and written, as much again of the targets' rows).
 constexpr int kPartSums = 8;
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_entropy_rows(RowArgs a) {
@@ -535,7 +539,7 @@ struct Logits {
   using S = Shape<kPair, 256, kOfGradient ? 4096 : 0>;
   // The tensor cores cut what an accumulator cannot hold, towards zero, at every 16 elements: sums
   // over 4096 elements gave losses 0.9e-6 off, over 8192 2.7e-6. Wider rows (kLongSums) are
-  // summed 2048 elements at a time. (Up to there each group of warps takes a whole tile: 271 tokens,
+  // summed 2048 elements at a time. (A logit of 15 that is not the target's is then off by 7e-5 at most. Up to there each group of warps takes a whole tile: 271 tokens,
   // 50001 x 1031, 45 us instead of 58.) Logits of 15 in fp16 gradients show it from 8192 elements on: up to there
   // 0.00021 of the norm became 0.00023, at 32768 0.00044 (kLongGradient: 0.00021). bf16 ones do not.
   static constexpr int kChunk = kKind == kLongSums || kKind == kLongGradient ? 32 : 0;
