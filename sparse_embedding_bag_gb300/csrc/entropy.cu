@@ -539,9 +539,10 @@ struct Logits {
   using S = Shape<kPair, 256, kOfGradient ? 4096 : 0>;
   // The tensor cores cut what an accumulator cannot hold, towards zero, at every 16 elements: sums
   // over 4096 elements gave losses 0.9e-6 off, over 8192 2.7e-6. Wider rows (kLongSums) are
-  // summed 2048 elements at a time. (A logit of 15 that is not the target's is then off by 7e-5 at most. Up to there each group of warps takes a whole tile: 271 tokens,
-  // 50001 x 1031, 45 us instead of 58.) Logits of 15 in fp16 gradients show it from 8192 elements on: up to there
-  // 0.00021 of the norm became 0.00023, at 32768 0.00044 (kLongGradient: 0.00021). bf16 ones do not.
+  // summed 2048 elements at a time. (Up to there each group of warps takes a whole tile: 271 tokens,
+  // 50001 x 1031, 45 us instead of 58.) A logit of 15 that is not the target's is then off by 7e-5 at most.
+  // fp16 gradients show such logits from 8192 elements on: up to there 0.00021 of the norm became 0.00023,
+  // at 32768 0.00044 (kLongGradient: 0.00021). bf16 ones do not.
   static constexpr int kChunk = kKind == kLongSums || kKind == kLongGradient ? 32 : 0;
   const Args& a;
   uint32_t m_tiles, step, t, tiles;  // fewer than 2^29: divisions of 32 bits, between two tiles' MMAs
@@ -665,10 +666,7 @@ struct Logits {
       for (int c = 0; c < 128; c += 64) {
         const int32_t at = (int32_t)group * 128 + c;
         if (at >= a.cols) continue;
-        float x[2][32];
-#pragma unroll
-        for (int i = 0; i < 64; ++i) x[i / 32][i % 32] = v[c + i];
-        leave(maps, r, x, at, lane, aside, ok);
+        leave(maps, r, *reinterpret_cast<float (*)[2][32]>(v + c), at, lane, aside, ok);
       }
       return;
     }
@@ -838,8 +836,9 @@ struct GradArgs {
 };
 
 // The long sums (dh) come first, one or more a group; groups that have one fewer take
-// as many more tiles of dW first as that sum is long, the rest goes round. kLong: sums over more than
-// most_summed() tokens, added up in registers.
+// as many more tiles of dW first as that sum is long, the rest goes round. kLong: dW alone, from sums over
+// more than most_summed() tokens, added up in registers. (With dh's tiles among them, whose way out takes the
+// registers that hold the sums: 70000 tokens of 8000 x 4096 bf16 18.5 ms, 6.3 apart.)
 template <typename T, bool kPair, bool kLong>
 struct Grads {
   static constexpr int kChunk = kLong ? most_summed(std::is_same<T, __half>::value) / kDepth : 0;
@@ -858,7 +857,7 @@ struct Grads {
     count = rows_of_g(*a.count, a.second);
     pad = (count + S::kRows - 1) / S::kRows * S::kRows;
     splits = splits_of<kPair>(a.split, count, groups);
-    tiles_h = a.want_h ? pad / S::kRows * a.split.d_tiles : 0;
+    tiles_h = !kLong && a.want_h ? pad / S::kRows * a.split.d_tiles : 0;
     units_h = tiles_h * splits;
     kh = (a.V1 - a.V0 + kDepth - 1) / kDepth, kw = (count + kDepth - 1) / kDepth;
     tiles_w = a.want_t ? (a.V1 - a.V0 + S::kRows - 1) / S::kRows * a.split.d_tiles : 0;
@@ -925,7 +924,7 @@ struct Grads {
   __device__ int32_t cols() const { return min(kCols, (over_tokens ? a.D : a.split.Dp) - col0); }
   // Columns c..c+63 of the tile.
   __device__ void leave(const Maps& maps, float (&v)[2][32], int32_t row, int32_t c, uint32_t lane, uint8_t* aside) const {
-    if (!over_tokens) {  // Dp is a multiple of 64
+    if (!kLong && !over_tokens) {  // Dp is a multiple of 64
       float* acc = a.acc + ((int64_t)part * pad + row) * a.split.Dp + col0 + c;
 #pragma unroll
       for (int i = 0; i < 64; i += 4) {
@@ -975,9 +974,11 @@ struct Grads {
 #pragma unroll
     for (int c = 0; c < kCols / 2; c += 64) {
       if (first + c >= there) continue;
-      float x[2][32];
+      float (&x)[2][32] = *reinterpret_cast<float (*)[2][32]>(v + c);
+      if (!ok) {
 #pragma unroll
-      for (int i = 0; i < 64; ++i) x[i / 32][i % 32] = ok ? v[c + i] : NAN;
+        for (int i = 0; i < 64; ++i) x[i / 32][i % 32] = NAN;
+      }
       leave(maps, x, row, first + c, lane, aside);
     }
   }
@@ -1216,7 +1217,8 @@ cudaError_t run(const Call& c, const Layout& l) {
   if (e != cudaSuccess) return e;
   const int64_t first = c.V < l.piece ? c.V : l.piece;
   constexpr bool kHalf = std::is_same<T, __half>::value;
-  const SplitArgs split{l.d_tiles, Dp, !c.dtable, (int32_t)((first + 4 * kDepth - 1) / (4 * kDepth)),
+  const bool apart = c.dtable && N > most_summed(kHalf);  // dW in a launch of its own
+  const SplitArgs split{l.d_tiles, Dp, !c.dtable || apart, (int32_t)((first + 4 * kDepth - 1) / (4 * kDepth)),
                         (int32_t)((first + most_summed(kHalf) - 1) / most_summed(kHalf))};
   GradArgs ga{count, l.second, c.D, 0, 0, c.dhidden != nullptr, c.dtable != nullptr, true, wide, split,
               reinterpret_cast<float*>(w + l.acc), c.dtable, c.dtable_stride, scale, c.status};
@@ -1235,13 +1237,15 @@ cudaError_t run(const Call& c, const Layout& l) {
       e = launch_mm<Logits<T, kPair, kGradient>, kPair>(c.device, l.groups, logit_maps, la, c.s);
     if (e != cudaSuccess) return e;
     if constexpr (kPair) {
-      if (c.dtable && N > most_summed(kHalf)) {
+      if (apart) {
         e = launch_mm<Grads<T, true, true>, true>(c.device, l.groups, grad_maps, ga, c.s);
         if (e != cudaSuccess) return e;
-        continue;
+        if (!c.dhidden) continue;
+        ga.want_t = false;
       }
     }
     e = launch_mm<Grads<T, kPair, false>, kPair>(c.device, l.groups, grad_maps, ga, c.s);
+    ga.want_t = c.dtable != nullptr;
     if (e != cudaSuccess) return e;
   }
   if (c.dhidden) {
