@@ -27,7 +27,7 @@ caller clears it.
 Of these ``distill_loss``, ``rms_norm``, ``dropout`` and ``cross_entropy_loss`` take part in autograd, all but
 ``dropout`` once (second derivatives are refused) and in backward mode alone (tangents are refused). The other
 calls take tensors that require gradients, or carry tangents, as values, and what they return has no history. An
-``out`` counts as changed in place.
+``out`` counts as changed in place, and shares no memory with another tensor of the call but where that says so.
 """
 from __future__ import annotations
 
